@@ -22,6 +22,12 @@ Entry points (same names as the C ABI, without the ``wq_`` prefix):
   (the GPTQModel packed format)
 * ``mse_search(w, bits, group_size, maxshrink=0.2, grid=100, norm=2.4,
   patience=None, symmetric=False) -> dict`` (per-group s, z of the MSE observer)
+* ``moe_route(logits, top_k, renormalize=True, scale=1.0) -> (ids, weights)``,
+  ``moe(x, ids, weights, w_up, s_up, z_up, w_down, s_down, z_down, bits,
+  group_size, activation="silu") -> y`` and ``MoePlan`` (the same layer with its
+  weights bound once): a mixture-of-experts layer on packed weights
+* ``logprobs(logits, tokens=None, top_k=0) -> dict`` and
+  ``matmul_logprobs(x, ..., tokens, top_k)`` (the same behind ``matmul``)
 
 x, scales, zeros, bias and the output are all ``torch.float16`` or all
 ``torch.bfloat16`` (the type of x decides; bfloat16 sets ``WQ_FLAG_BF16``).
@@ -51,6 +57,9 @@ STATUS = {
 WQ_FLAG_PDL = 1
 WQ_FLAG_PDL_INPUTS_READY = 2
 WQ_FLAG_BF16 = 4
+MOE_MAX_TOKENS = 64
+MOE_MAX_EXPERTS = 512
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
 
 _lib = None
 
@@ -107,6 +116,14 @@ def lib() -> ctypes.CDLL:
         L.wq_gptq_workspace_size.restype = ctypes.c_size_t
         L.wq_gptq_quantize.argtypes = [p, p, p, p, i, i, i, i, i, ctypes.c_float, p, p, p, p, ctypes.c_size_t, p]
         L.wq_gptq_quantize.restype = i
+        L.wq_moe_route.argtypes = [p, i, i, i, ctypes.c_int64, i, i, ctypes.c_float, p, p, u, p]
+        L.wq_moe_route.restype = i
+        L.wq_moe_workspace_size.argtypes = [i, i, i, i]
+        L.wq_moe_workspace_size.restype = ctypes.c_size_t
+        L.wq_moe.argtypes = [p] * 10 + [i] * 9 + [u, p, ctypes.c_size_t, p]
+        L.wq_moe.restype = i
+        L.wq_logprobs.argtypes = [p, i, i, i, ctypes.c_int64, p, i, p, p, p, p, u, p]
+        L.wq_logprobs.restype = i
         for f in ("wq_pack_kmajor", "wq_unpack_kmajor", "wq_gemv", "wq_gemm", "wq_device_status",
                   "wq_selftest_wait_timeout"):
             getattr(L, f).restype = i
@@ -593,3 +610,194 @@ def gptqmodel_quantized_matmul(x, qweight, qzeros, scales, bits: int, group_size
     with GPTQModel operands, through ``from_gptqmodel`` and ``matmul``."""
     w_q, w_lo, zeros = from_gptqmodel(qweight, qzeros, bits, group_size, x.shape[1], dtype=_elem_type(x))
     return matmul(x, w_q, w_lo, scales, zeros, bits, group_size, out=out)
+
+
+# --------------------------------------------------- mixture of experts, log probabilities
+
+def _on_current(t, name: str):
+    """The library launches on the current device: a tensor of another one is refused."""
+    if t.get_device() != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_torch().cuda.current_device()}")
+
+
+def _logits(logits):
+    """Type, rows, columns and row stride of a 2-d tensor of logits, whose rows are contiguous."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
+    kind = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a 2-d tensor")
+    rows, cols = logits.shape
+    if cols > 1 and logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    ld = logits.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError("the rows of logits overlap")
+    _on_current(logits, "logits")
+    return kind, rows, cols, ld
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True, scale: float = 1.0, pdl: bool = False):
+    """``wq_moe_route``: the experts of each token and their weights.
+
+    ``logits``: (T, E) float16, bfloat16 or float32, E <= 512, rows contiguous
+    (any row stride).  Returns ``ids`` (T, top_k) int32, in the order (logit
+    descending, index ascending), and ``weights`` (T, top_k) float32: ``scale``
+    times the softmax over the chosen experts (``renormalize``) or over all of
+    them.  A logit of -inf or NaN is never chosen: where fewer than ``top_k``
+    experts are left the slot is empty, id -1 and weight 0."""
+    torch = _torch()
+    kind, T, E, ld = _logits(logits)
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    st = lib().wq_moe_route(logits.data_ptr(), kind, T, E, ld, top_k, 1 if renormalize else 0, float(scale),
+                            ids.data_ptr(), weights.data_ptr(), WQ_FLAG_PDL if pdl else 0, _stream())
+    _check("wq_moe_route", st)
+    return ids, weights
+
+
+class MoePlan:
+    """A mixture-of-experts layer with its packed weights bound once (``wq_moe``).
+
+    ``MoePlan(w_up, s_up, z_up, w_down, s_down, z_down, bits, group_size,
+    tokens, top_k, activation="silu", pdl=False)``: ``w_up`` (E, K / eps, 2 I)
+    int32 holds each expert's gate columns, then its up columns, ``w_down``
+    (E, I / eps, N), as ``pack_kmajor`` lays a weight out (a stack of experts
+    packs as one (E * K, N) code matrix); scales and zeros (E, K / G, 2 I) and
+    (E, I / G, N).  ``tokens``: the most tokens a call brings (at most 64).
+
+    ``plan(x, ids, weights, out=None)`` is then, for x (T, K), T <= tokens, and
+    ids and weights (T, top_k) as ``moe_route`` gives them,
+
+        y[t] = sum_j weights[t, j] * (act(x[t] @ Wg[e]) * (x[t] @ Wu[e])) @ Wd[e],  e = ids[t, j]
+
+    with act "silu" or "gelu".  An id outside 0 .. E-1 leaves its slot empty; a
+    token without slots gets zeros.  Two launches; each call takes a workspace of
+    its own from the caching allocator, so calls on several streams and captured
+    graphs do not share one.  The plan holds references to the weights, which
+    must not be resized or moved (their contents may change)."""
+
+    def __init__(self, w_up, s_up, z_up, w_down, s_down, z_down, bits: int, group_size: int, tokens: int,
+                 top_k: int, activation: str = "silu", pdl: bool = False):
+        torch = _torch()
+        dt = _elem_type(s_up)
+        if bits not in (4, 8):
+            raise ValueError(f"bits must be 4 or 8, got {bits}")
+        if activation not in _ACTIVATIONS:
+            raise ValueError(f"activation must be one of {tuple(_ACTIVATIONS)}, got {activation!r}")
+        if not 1 <= tokens <= MOE_MAX_TOKENS:
+            raise ValueError(f"tokens must be 1 to {MOE_MAX_TOKENS}, got {tokens}")
+        if not 1 <= top_k <= 16:
+            raise ValueError(f"top_k must be 1 to 16, got {top_k}")
+        for t, name in ((w_up, "w_up"), (w_down, "w_down")):
+            _need(t, torch.int32, name, ndim=3)
+        for t, name in ((s_up, "s_up"), (z_up, "z_up"), (s_down, "s_down"), (z_down, "z_down")):
+            _need(t, dt, name, ndim=3)
+        _same_device(w_up, s_up=s_up, z_up=z_up, w_down=w_down, s_down=s_down, z_down=z_down)
+        eps = _EPS[bits]
+        E, K, I, N = w_up.shape[0], w_up.shape[1] * eps, w_up.shape[2] // 2, w_down.shape[2]
+        if not 1 <= E <= MOE_MAX_EXPERTS:
+            raise ValueError(f"1 to {MOE_MAX_EXPERTS} experts, got {E}")
+        if w_up.shape[2] != 2 * I or w_down.shape[:2] != (E, I // eps) or I % eps:
+            raise ValueError(f"w_up has shape {tuple(w_up.shape)}, w_down {tuple(w_down.shape)}: needed are "
+                             f"(E, K / {eps}, 2 I) and (E, I / {eps}, N)")
+        for name, s, z, rows, cols in (("up", s_up, z_up, K, 2 * I), ("down", s_down, z_down, I, N)):
+            G = rows if group_size == -1 else group_size
+            if G < 1 or rows % G:
+                raise ValueError(f"group size {group_size} does not divide the {name} product's {rows} rows")
+            for t, what in ((s, "s"), (z, "z")):
+                if t.shape != (E, rows // G, cols):
+                    raise ValueError(f"{what}_{name} has shape {tuple(t.shape)}; needs {(E, rows // G, cols)}")
+        self._keep = (w_up, s_up, z_up, w_down, s_down, z_down)
+        self._weights = tuple(t.data_ptr() for t in self._keep)
+        flags = (WQ_FLAG_PDL if pdl else 0) | (WQ_FLAG_BF16 if dt is torch.bfloat16 else 0)
+        self._shape = (K, I, N, E, top_k, bits, group_size, _ACTIVATIONS[activation], flags)
+        self.dtype, self.device, self.tokens, self.top_k, self.K, self.N = dt, w_up.device, tokens, top_k, K, N
+        self._dev = w_up.get_device()
+        self._run = lib().wq_moe
+        self._bytes = [0] + [int(lib().wq_moe_workspace_size(T, top_k, I, N)) for T in range(1, tokens + 1)]
+
+    def __call__(self, x, ids, weights, out=None):
+        torch = _torch()
+        _need(x, self.dtype, "x")
+        _need(ids, torch.int32, "ids")
+        _need(weights, torch.float32, "weights")
+        T, d = x.shape[0], self._dev
+        if x.shape[1] != self.K or not 1 <= T <= self.tokens:
+            raise ValueError(f"x has shape {tuple(x.shape)}; needs (1 to {self.tokens}, {self.K})")
+        if ids.shape != (T, self.top_k) or weights.shape != (T, self.top_k):
+            raise ValueError(f"ids and weights have shapes {tuple(ids.shape)} and {tuple(weights.shape)}; "
+                             f"need {(T, self.top_k)}")
+        if out is None:
+            out = torch.empty((T, self.N), dtype=self.dtype, device=self.device)
+        else:
+            _need(out, self.dtype, "out")
+            if out.shape != (T, self.N):
+                raise ValueError(f"out has shape {tuple(out.shape)}; needs {(T, self.N)}")
+        if x.get_device() != d or ids.get_device() != d or weights.get_device() != d or out.get_device() != d:
+            raise ValueError(f"all tensors must be on the weights' device {self.device}")
+        _on_current(x, "x")
+        nbytes = self._bytes[T]
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        K, I, N, E, top_k, bits, group_size, act, flags = self._shape
+        st = self._run(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), *self._weights, out.data_ptr(), T, K, I, N,
+                       E, top_k, bits, group_size, act, flags, ws.data_ptr(), nbytes, _stream())
+        if st != 0:
+            raise WQError("wq_moe", st)
+        return out
+
+
+def moe(x, ids, weights, w_up, s_up, z_up, w_down, s_down, z_down, bits: int, group_size: int,
+        activation: str = "silu", out=None, pdl: bool = False):
+    """``wq_moe``: one mixture-of-experts layer for up to 64 tokens; ``MoePlan``
+    describes the arguments and keeps them for a layer that is applied often."""
+    _need(x, _elem_type(x), "x")
+    if getattr(ids, "ndim", 0) != 2:
+        raise ValueError("ids must be a (T, top_k) tensor")
+    return MoePlan(w_up, s_up, z_up, w_down, s_down, z_down, bits, group_size, x.shape[0], ids.shape[1],
+                   activation=activation, pdl=pdl)(x, ids, weights, out=out)
+
+
+def logprobs(logits, tokens=None, top_k: int = 0, pdl: bool = False):
+    """``wq_logprobs``: log probabilities of given tokens, the entropy and the
+    most probable alternatives of each row, in one pass over the logits.
+
+    ``logits``: (R, V) float16, bfloat16 or float32, rows contiguous (any row
+    stride); masked entries may be -inf or the type's lowest value.  ``tokens``:
+    (R,) int64, or None; one outside 0 .. V-1 (a padded row) has log probability
+    -inf.  Returns a dict: ``entropy`` (R,) float32; with tokens ``logprob`` (R,)
+    float32; with ``top_k`` (at most 32) ``top_logprob`` (R, top_k) float32 and
+    ``top_id`` (R, top_k) int64, in the order (logit descending, index
+    ascending).  A row of nothing but -inf, or with NaN or +inf, is NaN."""
+    torch = _torch()
+    kind, R, V, ld = _logits(logits)
+    if not 0 <= top_k <= min(V, 32):
+        raise ValueError(f"top_k must be 0 to {min(V, 32)}, got {top_k}")
+    dev = logits.device
+    out = {"entropy": torch.empty(R, dtype=torch.float32, device=dev)}
+    if tokens is not None:
+        _need(tokens, torch.int64, "tokens", ndim=1)
+        _same_device(logits, tokens=tokens)
+        if tokens.shape[0] != R:
+            raise ValueError(f"tokens has shape {tuple(tokens.shape)}; needs ({R},)")
+        out["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
+    if top_k:
+        out["top_logprob"] = torch.empty((R, top_k), dtype=torch.float32, device=dev)
+        out["top_id"] = torch.empty((R, top_k), dtype=torch.int64, device=dev)
+    st = lib().wq_logprobs(logits.data_ptr(), kind, R, V, ld, _ptr(tokens), top_k, _ptr(out.get("logprob")),
+                           out["entropy"].data_ptr(), _ptr(out.get("top_logprob")), _ptr(out.get("top_id")),
+                           WQ_FLAG_PDL if pdl else 0, _stream())
+    _check("wq_logprobs", st)
+    return out
+
+
+def matmul_logprobs(x, w_q, w_lo, scales, zeros, bits: int, group_size: int, tokens=None, top_k: int = 0, bias=None):
+    """The read-out of a decoder whose LM head is quantised: ``logprobs`` of the
+    logits ``matmul(x, ...)`` (in the type of x), launched as its dependent."""
+    logits = matmul(x, w_q, w_lo, scales, zeros, bits, group_size, bias=bias)
+    return logprobs(logits, tokens, top_k, pdl=True)

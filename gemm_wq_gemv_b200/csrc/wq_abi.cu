@@ -287,6 +287,79 @@ wq_status wq_gptq_quantize(const float* W, const float* H, const float* scale, c
                            workspace, (cudaStream_t)stream);
 }
 
+wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, int top_k, int renormalize,
+                       float scale, int32_t* ids, float* weights, unsigned flags, void* stream) {
+    if (type != WQ_TYPE_F16 && type != WQ_TYPE_BF16 && type != WQ_TYPE_F32) return WQ_ERR_UNSUPPORTED;
+    if (T < 1 || E < 1 || E > WQ_MOE_MAX_EXPERTS || ld < E || ld > (1ll << 40)) return WQ_ERR_INVALID_ARG;
+    if (top_k < 1 || top_k > 16 || top_k > E) return WQ_ERR_INVALID_ARG;
+    if (renormalize != 0 && renormalize != 1) return WQ_ERR_INVALID_ARG;
+    if (!(scale > -3.0e38f) || !(scale < 3.0e38f)) return WQ_ERR_INVALID_ARG;  // rejects NaN and infinities
+    if (flags & ~WQ_FLAG_PDL) return WQ_ERR_INVALID_ARG;
+    if (!logits || !ids || !weights) return WQ_ERR_INVALID_ARG;
+    if (!aligned(logits, type == WQ_TYPE_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4))
+        return WQ_ERR_ALIGNMENT;
+    wq_status st = check_device();
+    if (st != WQ_OK) return st;
+    return wq::launch_moe_route(logits, type, T, E, ld, top_k, renormalize, scale, ids, weights, flags,
+                                (cudaStream_t)stream);
+}
+
+size_t wq_moe_workspace_size(int T, int top_k, int inner, int N) {
+    if (T < 1 || T > WQ_MOE_MAX_TOKENS || top_k < 1 || top_k > 16 || inner < 1 || N < 1) return 0;
+    return wq::moe_layout(T, top_k, inner, N).bytes;
+}
+
+wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* w_up,
+                 const uint16_t* s_up, const uint16_t* z_up, const uint32_t* w_down, const uint16_t* s_down,
+                 const uint16_t* z_down, uint16_t* y, int T, int K, int inner, int N, int E, int top_k, int bits,
+                 int group_size, int activation, unsigned flags, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    if (bits != 4 && bits != 8) return WQ_ERR_UNSUPPORTED;
+    if (inner < 1 || inner > (1 << 29)) return WQ_ERR_INVALID_ARG;
+    wq_status st = check_plane_shape(K, 2 * inner, bits, nullptr, true);
+    if (st == WQ_OK) st = check_plane_shape(inner, N, bits, nullptr, true);
+    if (st != WQ_OK) return st;
+    if (T < 1 || T > WQ_MOE_MAX_TOKENS || top_k < 1 || top_k > 16) return WQ_ERR_INVALID_ARG;
+    if (E < 1 || E > WQ_MOE_MAX_EXPERTS) return WQ_ERR_INVALID_ARG;
+    if (activation != WQ_ACT_SILU && activation != WQ_ACT_GELU) return WQ_ERR_UNSUPPORTED;
+    if (flags & ~(WQ_FLAG_PDL | WQ_FLAG_BF16)) return WQ_ERR_INVALID_ARG;
+    if (!x || !ids || !weights || !w_up || !s_up || !z_up || !w_down || !s_down || !z_down || !y || !workspace)
+        return WQ_ERR_INVALID_ARG;
+    if (group_size != -1) {
+        if (group_size < 1 || K % group_size != 0 || inner % group_size != 0) return WQ_ERR_INVALID_ARG;
+        if (group_size % (4 * main_eps(bits)) != 0) return WQ_ERR_UNSUPPORTED;
+    }
+    if (inner % 8 != 0 || N % 8 != 0) return WQ_ERR_ALIGNMENT;
+    if (!aligned(x, 16) || !aligned(w_up, 16) || !aligned(s_up, 16) || !aligned(z_up, 16) || !aligned(w_down, 16) ||
+        !aligned(s_down, 16) || !aligned(z_down, 16) || !aligned(y, 16) || !aligned(ids, 4) ||
+        !aligned(weights, 4) || !aligned(workspace, 256))
+        return WQ_ERR_ALIGNMENT;
+    if (workspace_bytes < wq_moe_workspace_size(T, top_k, inner, N)) return WQ_ERR_INVALID_ARG;
+    if ((st = check_device()) != WQ_OK) return st;
+    const wq::MoeProblem m{x, ids, weights, w_up, s_up, z_up, w_down, s_down, z_down, y,
+                           T, top_k, E, K, inner, N, bits, group_size, activation, flags, workspace};
+    return wq::launch_moe(m, (cudaStream_t)stream);
+}
+
+wq_status wq_logprobs(const void* logits, int type, int R, int V, int64_t ld, const int64_t* tokens, int top_k,
+                      float* logprob, float* entropy, float* top_logprob, int64_t* top_id, unsigned flags,
+                      void* stream) {
+    if (type != WQ_TYPE_F16 && type != WQ_TYPE_BF16 && type != WQ_TYPE_F32) return WQ_ERR_UNSUPPORTED;
+    if (R < 1 || R > (1 << 24) || V < 1 || V >= (1 << 30) || ld < V || ld > (1ll << 40)) return WQ_ERR_INVALID_ARG;
+    if (top_k < 0 || top_k > 32 || top_k > V) return WQ_ERR_INVALID_ARG;
+    if (flags & ~WQ_FLAG_PDL) return WQ_ERR_INVALID_ARG;
+    if (!logits || !entropy || (tokens == nullptr) != (logprob == nullptr)) return WQ_ERR_INVALID_ARG;
+    if ((top_k > 0) != (top_logprob != nullptr) || (top_k > 0) != (top_id != nullptr)) return WQ_ERR_INVALID_ARG;
+    if (!aligned(logits, type == WQ_TYPE_F32 ? 4 : 2) || !aligned(entropy, 4) || (tokens && !aligned(tokens, 8)) ||
+        (logprob && !aligned(logprob, 4)) || (top_logprob && !aligned(top_logprob, 4)) ||
+        (top_id && !aligned(top_id, 8)))
+        return WQ_ERR_ALIGNMENT;
+    wq_status st = check_device();
+    if (st != WQ_OK) return st;
+    return wq::launch_logprobs(logits, type, R, V, ld, tokens, top_k, logprob, entropy, top_logprob, top_id, flags,
+                               (cudaStream_t)stream);
+}
+
 int wq_checked_build(void) {
 #ifdef WQ_CHECKS
     return 1;
@@ -300,9 +373,10 @@ wq_status wq_device_status(int reset) {
     const wq_status b = wq::gemv_device_status(reset);
     const wq_status c = wq::gemv_lean_device_status(reset);
     const wq_status d = wq::gptq_device_status(reset);
-    if (a == WQ_ERR_CUDA || b == WQ_ERR_CUDA || c == WQ_ERR_CUDA || d == WQ_ERR_CUDA) return WQ_ERR_CUDA;
-    for (const wq_status e : {WQ_ERR_TIMEOUT, WQ_ERR_CHECK})
-        if (a == e || b == e || c == e) return e;
+    const wq_status m = wq::moe_device_status(reset);
+    const wq_status l = wq::logprobs_device_status(reset);
+    for (const wq_status e : {WQ_ERR_CUDA, WQ_ERR_TIMEOUT, WQ_ERR_CHECK})
+        if (a == e || b == e || c == e || m == e || l == e || (e == WQ_ERR_CUDA && d == e)) return e;
     return d;
 }
 

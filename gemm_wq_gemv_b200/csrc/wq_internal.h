@@ -77,6 +77,37 @@ wq_status launch_gptq(const float* W, const float* H, const float* scale, const 
                       int bits, int blocksize, float percdamp, float* Q, uint8_t* codes, float* losses,
                       void* workspace, cudaStream_t s);
 
+// Mixture-of-experts layer (wq_moe.cu), arguments already validated.
+struct MoeProblem {
+    const uint16_t* x;
+    const int32_t* ids;
+    const float* weights;
+    const uint32_t* w_up;
+    const uint16_t* s_up;
+    const uint16_t* z_up;
+    const uint32_t* w_down;
+    const uint16_t* s_down;
+    const uint16_t* z_down;
+    uint16_t* y;
+    int T, top_k, E, K, I, N, bits, group_size, act;  // group_size -1: one group per column of each product
+    unsigned flags;
+    void* ws;
+};
+struct MoeLayout {
+    size_t off_h, off_part, bytes;
+};
+MoeLayout moe_layout(int T, int top_k, int I, int N);
+wq_status launch_moe(const MoeProblem& m, cudaStream_t s);
+wq_status moe_device_status(int reset);
+
+// Expert router (wq_route.cu) and token log probabilities (wq_logprobs.cu).
+wq_status launch_moe_route(const void* logits, int type, int T, int E, long long ld, int top_k, int renormalize,
+                           float scale, int32_t* ids, float* weights, unsigned flags, cudaStream_t s);
+wq_status launch_logprobs(const void* logits, int type, int R, int V, long long ld, const int64_t* tokens, int top_k,
+                          float* logprob, float* entropy, float* top_logprob, int64_t* top_id, unsigned flags,
+                          cudaStream_t s);
+wq_status logprobs_device_status(int reset);
+
 // 2-D tiled TMA descriptor for a row-major (outer, inner) array.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);

@@ -369,6 +369,96 @@ wq_status wq_gemv_plan_run(const wq_gemv_plan* plan, const uint16_t* x, uint16_t
 void wq_gemv_plan_destroy(wq_gemv_plan* plan);
 
 /*
+ * Operators around the products of a quantised decoder.  The pages have no
+ * counterpart: they end at the product.  `type` names the element type of an
+ * array of logits.
+ */
+#define WQ_TYPE_F16 0
+#define WQ_TYPE_BF16 1
+#define WQ_TYPE_F32 2
+
+/*
+ * Expert router: for each of T rows of logits l (one per expert) the top_k
+ * experts and their weights.
+ *   logits       (T, E), row stride ld >= E in elements, of `type`, aligned to
+ *                its element size.
+ *   ids          (T, top_k) int32 output: the experts in the order (logit
+ *                descending, index ascending).  A logit of -inf or NaN is never
+ *                chosen: where fewer than top_k experts are left the slot holds
+ *                -1 and the weight 0, the empty slot of wq_moe.
+ *   weights      (T, top_k) fp32 output: scale * exp(l_e - max) / sum, the sum over
+ *                the chosen experts (renormalize = 1) or over all E (0): the
+ *                softmax.  A NaN (or +inf) among a row's logits makes its weights NaN.
+ * 1 <= E <= WQ_MOE_MAX_EXPERTS, 1 <= top_k <= min(E, 16), scale finite.  fp32
+ * throughout.  flags: 0 or WQ_FLAG_PDL (the kernel may be launched while the
+ * previous one still runs; it reads its inputs after that one has completed).
+ */
+#define WQ_MOE_MAX_EXPERTS 512
+wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, int top_k, int renormalize,
+                       float scale, int32_t* ids, float* weights, unsigned flags, void* stream);
+
+/*
+ * A mixture-of-experts layer on packed weights, for a few tokens:
+ *   h[t][j] = act(x[t] @ Wg[e]) * (x[t] @ Wu[e]),  e = ids[t][j]
+ *   y[t]    = sum_j weights[t][j] * (h[t][j] @ Wd[e])
+ * in two launches; each chosen expert's words are read once.
+ *   x        (T, K), y (T, N): binary16, or bfloat16 with WQ_FLAG_BF16, as all s and z.
+ *   ids      (T, top_k) int32, weights (T, top_k) fp32: as wq_moe_route writes
+ *            them.  An id outside 0 .. E-1 leaves its slot empty; a token whose
+ *            slots are all empty gets zeros.  An expert may occur in several
+ *            slots of a token.
+ *   w_up     (E, K/eps, 2*inner) K-major words: the gate's `inner` columns, then
+ *            the up projection's;  s_up, z_up (E, K/G, 2*inner).
+ *   w_down   (E, inner/eps, N) words;  s_down, z_down (E, inner/G, N).
+ *   activation  WQ_ACT_SILU: g / (1 + exp(-g)); WQ_ACT_GELU: g * Phi(g), the exact form.
+ *   workspace   wq_moe_workspace_size() bytes of device memory, 256-byte aligned,
+ *            any contents; calls that may run at the same time must not share it.
+ * Sums are fp32; h is kept as a pair of bfloat16 (16 significant bits, fp32's
+ * range); y is rounded once.  The result does not depend on timing: slots are
+ * summed in order.  Values of x have to be finite (else the rows that hold
+ * others become NaN or infinite; no other row does).
+ * bits 4 or 8 (else WQ_ERR_UNSUPPORTED).  1 <= T <= WQ_MOE_MAX_TOKENS,
+ * 1 <= top_k <= 16, 1 <= E <= WQ_MOE_MAX_EXPERTS.  K and inner multiples of eps
+ * and of the group size (-1: one group per column), the group size a multiple
+ * of 4 * eps as for wq_gemv; inner and N multiples of 8.  Arrays of 16-bit
+ * values and words 16-byte aligned, ids and weights 4-byte.  flags:
+ * WQ_FLAG_BF16, WQ_FLAG_PDL (all inputs are read after the previous kernel on
+ * the stream has completed).
+ */
+#define WQ_MOE_MAX_TOKENS 64
+#define WQ_MOE_MAX_SLOTS (WQ_MOE_MAX_TOKENS * 16)
+#define WQ_ACT_SILU 0
+#define WQ_ACT_GELU 1
+size_t wq_moe_workspace_size(int T, int top_k, int inner, int N);
+wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* w_up,
+                 const uint16_t* s_up, const uint16_t* z_up, const uint32_t* w_down, const uint16_t* s_down,
+                 const uint16_t* z_down, uint16_t* y, int T, int K, int inner, int N, int E, int top_k, int bits,
+                 int group_size, int activation, unsigned flags, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/*
+ * Log probabilities behind a read-out: for each of R rows of logits l over a
+ * vocabulary of V,
+ *   logprob     (R,) fp32: l[token] - lse, lse = log sum exp l; -inf for a token
+ *               outside 0 .. V-1 (a padded row).
+ *   entropy     (R,) fp32: -sum p log p, p = exp(l - lse), 0 log 0 = 0.
+ *   top_logprob, top_id  (R, top_k) fp32 / int64: the top_k most probable
+ *               entries in the order (logit descending, index ascending); a NaN
+ *               orders as -inf.
+ *   logits      (R, V) of `type`, row stride ld >= V in elements, aligned to its
+ *               element size.
+ *   tokens      (R,) int64 and logprob: both given, or both NULL.
+ *   top_logprob, top_id  given if top_k > 0, else NULL.
+ * One pass over the logits in fp32.  Masked entries may be -inf or the type's
+ * lowest value.  A row that holds NaN or +inf, or nothing but -inf, has NaN
+ * logprob (of a token inside the vocabulary), entropy and top_logprob.  1 <= R <= 2^24, 1 <= V < 2^30, 0 <= top_k <=
+ * min(V, 32).  flags: 0 or WQ_FLAG_PDL, as wq_moe_route.
+ */
+wq_status wq_logprobs(const void* logits, int type, int R, int V, int64_t ld, const int64_t* tokens, int top_k,
+                      float* logprob, float* entropy, float* top_logprob, int64_t* top_id, unsigned flags,
+                      void* stream);
+
+/*
  * Device-side status of the current device: WQ_OK, or WQ_ERR_TIMEOUT when a
  * kernel on this device gave up a bounded wait since the last reset (its
  * output is then incomplete), or WQ_ERR_CHECK when a bounds check of the
