@@ -306,7 +306,7 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
 
 size_t wq_moe_workspace_size(int T, int top_k, int inner, int N) {
     if (T < 1 || T > WQ_MOE_MAX_TOKENS || top_k < 1 || top_k > 16 || inner < 1 || N < 1) return 0;
-    return wq::moe_layout(T, top_k, inner, N).bytes;
+    return wq::moe_workspace_bytes(T, top_k, inner);
 }
 
 wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* w_up,
@@ -327,8 +327,9 @@ wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, co
         return WQ_ERR_INVALID_ARG;
     if (group_size != -1) {
         if (group_size < 1 || K % group_size != 0 || inner % group_size != 0) return WQ_ERR_INVALID_ARG;
-        if (group_size % (4 * main_eps(bits)) != 0) return WQ_ERR_UNSUPPORTED;
+        if (group_size % 32 != 0) return WQ_ERR_UNSUPPORTED;
     }
+    if (K > WQ_MOE_MAX_K) return WQ_ERR_UNSUPPORTED;
     if (inner % 8 != 0 || N % 8 != 0) return WQ_ERR_ALIGNMENT;
     if (!aligned(x, 16) || !aligned(w_up, 16) || !aligned(s_up, 16) || !aligned(z_up, 16) || !aligned(w_down, 16) ||
         !aligned(s_down, 16) || !aligned(z_down, 16) || !aligned(y, 16) || !aligned(ids, 4) ||

@@ -67,6 +67,47 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t 
     return true;
 }
 
+// A per-thread cache like make_map's, with its own key.
+bool make_map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint32_t elem, int dims, uint64_t cols,
+                   uint64_t planes, uint64_t rows, uint32_t box_cols, uint32_t box_planes, uint32_t box_rows,
+                   CUtensorMapSwizzle sw) {
+    struct Key {
+        const void* ptr;
+        uint64_t cols, planes, rows;
+        uint32_t elem, box_cols, box_planes, box_rows;
+        int dims, dt, sw;
+        bool operator==(const Key& o) const {
+            return ptr == o.ptr && cols == o.cols && planes == o.planes && rows == o.rows && elem == o.elem &&
+                   box_cols == o.box_cols && box_planes == o.box_planes && box_rows == o.box_rows && dims == o.dims &&
+                   dt == o.dt && sw == o.sw;
+        }
+    };
+    struct Entry {
+        Key key;
+        CUtensorMap map;
+        bool valid;
+    };
+    static thread_local Entry cache[MAP_CACHE];
+    const Key key{ptr, cols, planes, rows, elem, box_cols, box_planes, box_rows, dims, (int)dt, (int)sw};
+    const size_t h = ((reinterpret_cast<uintptr_t>(ptr) >> 8) ^ (cols * 31) ^ (rows * 131) ^ (box_rows * 7) ^
+                      (uint64_t)dt) % MAP_CACHE;
+    if (cache[h].valid && cache[h].key == key) {
+        *m = cache[h].map;
+        return true;
+    }
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t extent[3] = {cols, dims == 3 ? planes : rows, rows};
+    cuuint64_t strides[2] = {dims == 3 ? cols * elem : planes * cols * elem, planes * cols * elem};
+    cuuint32_t box[3] = {box_cols, dims == 3 ? box_planes : box_rows, box_rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    if (fn(m, dt, dims, const_cast<void*>(ptr), extent, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    cache[h] = Entry{key, *m, true};
+    return true;
+}
+
 // Unique ID of the CUDA context current on this thread (0 when there is none or
 // the driver does not report one).  A context that is destroyed and created
 // again (cudaDeviceReset) gets a new ID, so per-context state keyed on it --

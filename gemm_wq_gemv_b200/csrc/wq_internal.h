@@ -93,10 +93,7 @@ struct MoeProblem {
     unsigned flags;
     void* ws;
 };
-struct MoeLayout {
-    size_t off_h, off_part, bytes;
-};
-MoeLayout moe_layout(int T, int top_k, int I, int N);
+size_t moe_workspace_bytes(int T, int top_k, int I);
 wq_status launch_moe(const MoeProblem& m, cudaStream_t s);
 wq_status moe_device_status(int reset);
 
@@ -111,6 +108,10 @@ wq_status logprobs_device_status(int reset);
 // 2-D tiled TMA descriptor for a row-major (outer, inner) array.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// The same for rows made of `planes` planes of `cols` elements each (2 or 3 dimensions).
+bool make_map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint32_t elem, int dims, uint64_t cols,
+                   uint64_t planes, uint64_t rows, uint32_t box_cols, uint32_t box_planes, uint32_t box_rows,
+                   CUtensorMapSwizzle sw);
 int sm_count();
 
 constexpr int MAX_DEVICES = 64;

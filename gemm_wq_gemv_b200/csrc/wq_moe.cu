@@ -7,34 +7,48 @@
 // with W = (q - z) * s as everywhere in this library.  A slot whose id lies
 // outside 0 .. E-1 is empty and adds nothing.
 //
-// Two launches of one kernel template.  UP turns x into h; DOWN turns h into
-// one fp32 row per slot, and the last CTA of a column tile to finish sums the
-// slots of each token, in slot order, and writes y.  Both are bound by HBM: the
-// layer reads each chosen expert's words once.
-//  * Work split.  Slots are grouped by expert into blocks of BT slots, so an
-//    expert's words are read once for all its tokens.  The grid is (column
-//    tiles, an upper bound of the number of blocks); every CTA derives its block
-//    from the ids and the surplus CTAs leave.  A CTA owns 64 columns (UP: 32
-//    gate and the matching 32 up columns, so the activation needs no second
-//    pass) and its 8 warps split K; partials meet in shared memory.
-//  * Loads.  A warp walks its K range in quads (4 word rows) through a private
-//    ring of stages filled by cp.async: lane (g, t) (g = lane / 4, t = lane % 4)
-//    copies the 16 bytes (4 columns of word row 4 q + t) that it will itself
-//    convert, so words need no barrier and meet no bank conflict; only s and z,
-//    copied where a group starts, are read across lanes.
-//  * Products (m16n8k16 warp MMA, fp32 accumulators): A holds codes, B the
-//    tokens.  A code needs only AND / OR to become an operand: in fp16 the code
-//    bits are the subnormal q 2^-24, which the tensor core multiplies exactly; in
-//    bf16 4-bit codes are ORed into 128 (0x4300) and 8-bit ones go through fp32.
-//    One more MMA per k step with A = 1 gives X, the tokens' sums over the group,
-//    so a zero point of any value costs nothing per code: with D the group's
-//    product, acc += s (D - (128 + z) X) in fp32 (no 128 in fp16).
-//  * h is kept as two bf16 values, h = hi + lo (16 significant bits: 2^-17
-//    relative, far below the output's own rounding, and fp32's range, so an fp16
-//    layer cannot overflow between the products).  hi and lo of a token are two
-//    adjacent columns of the MMA, whose sum the fold takes.
-//  * DOWN is a programmatic dependent of UP: it finds its block and requests its
+// Two launches of one kernel template.  UP turns x into h (one row per slot),
+// DOWN turns h into y.  Both are meant to be bound by HBM: the layer reads
+// each chosen expert's words once.
+//  * Work split.  Slots are grouped by expert into blocks of bt slots (up to 8;
+//    fewer when K is very long), so an expert's words are read once for them.
+//    Every CTA (16 warps, one per SM) derives the blocks from the ids.  UP: the
+//    (block, column tile) pairs, all of K each, are dealt out over the SMs in equal
+//    runs.  DOWN: a column tile belongs to a cluster of up to 8 CTAs, among which the
+//    tile's (block, part of K) line is dealt out; they sum y, weighted, in shared
+//    memory and join the sums through distributed shared memory, in a fixed order.
+//    (Rows per slot in global memory, summed by the last CTA to arrive, cost 1 us
+//    per item for the fence and up to 17 us at the end.)  A CTA's warps are WK along
+//    K times 16 / WK along the columns, 64 columns each (UP: 32 gate and the matching
+//    32 up columns, so the activation needs no second pass); their partials meet in
+//    shared memory while the loads of the next item run.
+//  * Products on integers.  Unpacking codes to fp16 or bf16 costs 7 instructions
+//    per word of 8 codes, and with m16n8k16 (2.1 clocks per SM on B200) that held
+//    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
+//    bytes with 3 instructions per word, 8-bit codes are used as they are, and
+//    m16n8k32 on u8 x s8 (2.1 clocks too, twice the work) sums them exactly in int32.
+//  * x (or h) becomes 16-bit fixed point: per token and block of 128 values
+//    (aligned in K) a power-of-two step that puts the largest value at 2^14 to
+//    2^15, held as two signed bytes, which are two adjacent columns of the MMA:
+//    x = step * (256 hi + lo).  Error: half a step, at most 2^-15 of the block's
+//    largest value, none for values whose own last bit is at or above the step
+//    (a bf16 within 2^-7 of the largest, an fp16 within 2^-4); random over the
+//    block, so a product moves by about 3e-5 of itself, a tenth of the rounding of
+//    an fp16 output.  UP converts x once per block of slots, while its first words
+//    arrive, and leaves h converted (a tile's 128 values of a slot, or 64, are one
+//    block), so that DOWN copies bytes.  A block with a value that is not finite gets the step NaN.
+//  * One more MMA per step with A = 1 gives X, the tokens' sums, so that a zero
+//    point of any value costs nothing per code.  At the end of a block (or group):
+//    acc += s * step * (D - z X) in fp32, D = 256 D_hi + D_lo.
+//  * Loads.  A warp's words come by TMA, 16 word rows x 64 columns per stage (4 KB)
+//    with the s and z rows of its groups, into a private ring of two stages: 64 to
+//    128 KB in flight per SM.  The 128-byte swizzle and the column order of the
+//    lanes (chunk cg) keep the 16-byte reads free of bank conflicts.  (cp.async by every lane, which
+//    this replaced, cost 19 instructions per step of 32 values, a quarter of all.)
+//  * DOWN is a programmatic dependent of UP: it finds its blocks and requests its
 //    first words while UP drains, and waits only before it reads h.
+// Every mbarrier wait is bounded; on time-out the kernel records it in its status
+// word and skips the rest of the warp's work.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,183 +61,253 @@
 
 namespace wq {
 
-// Device status of these kernels: bit 1 once a check of the checked build failed.
+// Device status of these kernels: bit 0 once a bounded wait ran out, bit 1 once a
+// check of the checked build failed.
 __device__ unsigned int g_moe_status = 0;
 
 namespace {
 
-constexpr int MW = 8;           // warps per CTA, split along K
-constexpr int MT = MW * 32;
-constexpr int MCOLS = 64;       // weight columns per CTA (two halves of 32)
-constexpr int SZ_BYTES = 256;   // s and z of the 64 columns, one group
-constexpr int W_BYTES = 1024;   // one quad: 4 word rows x 64 columns
+constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
+constexpr int MAXBT = 8;        // slots per block
+#ifndef FEW_TILES
+#define FEW_TILES 300
+#endif
+constexpr int SK = 32;          // values of K per step (one MMA)
+constexpr int XBLK = 4;         // steps per block of fixed-point values
+constexpr int BOX_ROWS = 16;    // word rows per TMA box
+constexpr int STAGE = 2 * BOX_ROWS * 128;   // bytes: two halves
+constexpr int NST = 2;          // ring stages per warp
+constexpr uint64_t WAIT_NS = 2000000000ull;
+
+template <int BITS> constexpr int step_rows() { return SK * BITS / 32; }   // word rows per step: 4 or 8
 
 struct MoeParams {
-    const uint16_t* x;      // UP: (T, K); DOWN: null
-    uint16_t* h;            // (2, S, I) bf16: hi, then lo
+    const uint16_t* x;      // UP: (T, K)
+    int8_t* hq;             // (S, 2, Qh * SK): h in fixed point, hi then lo bytes, in the byte order of DOWN's MMA
+    float* hstep;           // (S, Qh): its steps, one per hb steps of K
     const int32_t* ids;     // (T, top_k)
     const float* weights;   // (T, top_k)
-    const uint32_t* w;      // (E, Kw, NW) words of this product
-    const uint16_t* s;      // (E, groups, NW)
-    const uint16_t* z;
-    float* part;            // (S, N): DOWN's rows per slot
-    unsigned int* count;    // arrivals per DOWN column tile
     uint16_t* y;            // (T, N)
-    int T, top_k, S, E;
+    int T, top_k, S, E, bt; // bt: slots per block
     int K;                  // inner length of this product (UP: K of x, DOWN: I)
     int NW;                 // weight columns (UP: 2 I, DOWN: N)
-    int NC;                 // columns the tiles cover (UP: I, DOWN: N)
     int I;
-    int Kw, Q, QW;          // word rows, quads, quads per warp
-    int qpg;                // quads per group (large when one group spans K)
+    int ntiles;             // column tiles
+    int Kw, Q;              // word rows, steps
+    int spg;                // steps per group (large when one group spans K)
     int groups;
+    int sz_rows;            // s (and z) rows per stage
     int act;
-    int ntiles_down;
+    int xcol;               // UP: bytes between two columns of x's fixed-point values
+    int nsteps;             // UP: fixed-point blocks of x
+    int Qh, hb;             // steps of K in a row of h; steps of K per fixed-point block of h (4 or 2)
+    int cluster;            // DOWN: CTAs per column tile
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void sts64(uint32_t dst, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(a), "r"(b) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void sts32(uint32_t dst, uint32_t a) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(a) : "memory");
 }
 
-// The block of a CTA: up to BT slots of one expert.
-struct Block {
-    int e, m, nblocks;  // expert, slots in the block, blocks in the whole launch
-};
+// 3-D tiled bulk tensor load into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_3d_u32(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+        "[%2];" ::"r"(dst),
+        "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 
-struct Lists {
-    int slots[MW][16];   // per warp: the block's slots (S <= 32), or row 0 for the whole CTA
-    int found[2];        // expert and slot count of the block
-    int total;
-};
-// Scratch of find_block while the ring holds nothing yet: slots per expert, the ids.
-struct Counts {
-    int cnt[WQ_MOE_MAX_EXPERTS];
-    int ids[WQ_MOE_MAX_SLOTS];
-};
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 
-// Block u of the launch: experts in the order of their first slot (S <= 32) or
-// of their number, slots in ascending order, BT per block.  Every warp gets
-// the result; the slots are in l.slots[warp] or, S > 32, l.slots[0].
-template <int BT>
-__device__ __forceinline__ Block find_block(const MoeParams& p, int u, Lists& l, Counts& c) {
+// D(16x8, s32) = A(16x32, u8) * B(32x8, s8) + D, or + c in every element (first).
+__device__ __forceinline__ void mma_u8s8(bool first, int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint2 b, int c) {
+    if (first)   // a constant where this is called
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "r"(c));
+    else
+        asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// The blocks of a launch: experts in the order of their first slot (S <= 32) or of their
+// number, up to bt slots each, in the order of the slots.
+struct Head {
+    int n;              // blocks
+    int i0, i1;         // this CTA's share
+};
+struct Blocks {         // in shared memory
+    Head* h;
+    int* start;         // sum of the weights of the blocks before u, and of all
+    int16_t* e;         // expert of block u
+    int16_t* first;     // its first slot's place in `order`
+    int16_t* order;     // the slots, block by block
+    // slots of block u
+    __device__ __forceinline__ int count(int u) const { return first[u + 1] - first[u]; }
+};
+__host__ __device__ constexpr int table_slots(int S) { return S < 32 ? 32 : S; }
+__host__ __device__ constexpr int table_bytes(int S) { return ((table_slots(S) + 1) * 4 + (3 * table_slots(S) + 1) * 2 + 15) / 16 * 16; }
+
+// Weight of a block of m slots: an item with two token tiles took 1.36 times as long (14.5 us against
+// 10.7 us for 4096 x 256 4-bit columns).
+__device__ __forceinline__ int block_weight(int m) { return m <= 4 ? 3 : 4; }
+
+// Work is dealt out along a line: block u takes `units` of it (UP: its column tiles, DOWN: its fixed-point
+// blocks of K), each as heavy as the block's weight.  The first unit at or after part i of n, by a whole warp.
+__device__ __forceinline__ int share(const Blocks& b, int units, int i, int n) {
+    const int lane = threadIdx.x & 31;
+    const int C = b.start[b.h->n] * units;                       // below 2^31 (checked by the host)
+    const int c = C / n * i + C % n * i / n;                  // floor(C i / n) in 32 bits
+    const int q = c / units;
+    int u = -1;
+    for (int v0 = 0; v0 < b.h->n; v0 += 32)
+        u += __popc(__ballot_sync(0xffffffffu, v0 + lane < b.h->n && b.start[v0 + lane] <= q));
+    const int w = b.start[u + 1] - b.start[u];
+    return u * units + (c - b.start[u] * units + w - 1) / w;
+}
+
+// This CTA's share, by one warp, from the complete table: part `i` of `n`.
+__device__ __forceinline__ void share_out(const Blocks& b, int units, int i, int n) {
+    int i0 = 0, i1 = 0;
+    if (b.h->n > 0) {
+        i0 = share(b, units, i, n);
+        i1 = share(b, units, i + 1, n);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        b.h->i0 = i0;
+        b.h->i1 = i1;
+    }
+}
+
+// Fills the table and this CTA's share; every thread returns after both are complete.  cnt: scratch, E ints.
+template <int MT>
+__device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b, int* cnt, int units, int part,
+                                            int parts) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned lt = (1u << lane) - 1u;
-    Block b;
-    if (p.S <= 32) {  // one slot per lane: no shared counts and no CTA barrier
-        const int id = lane < p.S ? p.ids[lane] : -1;
-        const bool valid = id >= 0 && id < p.E;
-        const unsigned same = __match_any_sync(0xffffffffu, valid ? id : -1 - lane);
-        const bool leader = valid && (same & lt) == 0;
-        const int nb = leader ? (__popc(same) + BT - 1) / BT : 0;
-        int pre = nb;
+    if (p.S <= 32) {   // one slot per lane of one warp
+        if (warp == 0) {
+            int id = lane < p.S ? p.ids[lane] : -1;
+            if (id >= p.E || id < 0) id = -1;
+            const unsigned same = __match_any_sync(0xffffffffu, id < 0 ? -1 - lane : id);
+            const bool leader = id >= 0 && (same & lt) == 0;
+            const int nb = leader ? (__popc(same) + p.bt - 1) / p.bt : 0;
+            const int m = leader ? __popc(same) : 0;
+            const int wt = leader ? (nb - 1) * block_weight(p.bt) + block_weight(m - (nb - 1) * p.bt) : 0;
+            int pre = nb, cost = wt, place = m;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, pre, d);
-            if (lane >= d) pre += v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, pre, d), c = __shfl_up_sync(0xffffffffu, cost, d);
+                const int l = __shfl_up_sync(0xffffffffu, place, d);
+                if (lane >= d) {
+                    pre += v;
+                    cost += c;
+                    place += l;
+                }
+            }
+            if (lane == 31) {
+                b.h->n = pre;
+                b.start[pre] = cost;
+                b.first[pre] = (int16_t)place;
+            }
+            pre -= nb;
+            cost -= wt;
+            place -= m;
+            for (int i = 0; i < nb; ++i) {
+                b.e[pre + i] = (int16_t)id;
+                b.first[pre + i] = (int16_t)(place + i * p.bt);
+                b.start[pre + i] = cost + i * block_weight(p.bt);
+            }
+            const int at = __shfl_sync(0xffffffffu, place, __ffs(same) - 1) + __popc(same & lt);
+            if (id >= 0) b.order[at] = (int16_t)lane;
+            __syncwarp();
+            share_out(b, units, part, parts);
         }
-        b.nblocks = __shfl_sync(0xffffffffu, pre, 31);
-        pre -= nb;
-        const unsigned hit = __ballot_sync(0xffffffffu, u >= pre && u < pre + nb);
-        if (hit == 0) {
-            b.e = b.m = 0;
-            return b;
-        }
-        const int src = __ffs(hit) - 1;
-        b.e = __shfl_sync(0xffffffffu, id, src);
-        const unsigned mine = __shfl_sync(0xffffffffu, same, src);
-        const int first = BT * (u - __shfl_sync(0xffffffffu, pre, src));
-        b.m = min(BT, __popc(mine) - first);
-        const int r = __popc(mine & lt) - first;
-        if (((mine >> lane) & 1u) && r >= 0 && r < BT) l.slots[warp][r] = lane;
-        __syncwarp();
-        return b;
+        __syncthreads();
+        return;
     }
-    for (int e = threadIdx.x; e < p.E; e += MT) c.cnt[e] = 0;
-    if (threadIdx.x < 2) l.found[threadIdx.x] = 0;
+    for (int e = threadIdx.x; e < p.E; e += MT) cnt[e] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < p.S; i += MT) {
         const int id = p.ids[i];
-        c.ids[i] = id;
-        if (id >= 0 && id < p.E) atomicAdd(&c.cnt[id], 1);
+        if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
     }
     __syncthreads();
     if (warp == 0) {
         const int per = (p.E + 31) / 32;
-        int mine = 0;
+        int mine = 0, wt = 0, m = 0;
         for (int j = 0; j < per; ++j) {
             const int e = lane * per + j;
-            mine += e < p.E ? (c.cnt[e] + BT - 1) / BT : 0;
+            if (e >= p.E) break;
+            m += cnt[e];
+            for (int r = 0; r < cnt[e]; r += p.bt) {
+                ++mine;
+                wt += block_weight(min(p.bt, cnt[e] - r));
+            }
         }
-        int pre = mine;
+        int pre = mine, cost = wt, place = m;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, pre, d);
-            if (lane >= d) pre += v;
+            const int v = __shfl_up_sync(0xffffffffu, pre, d), c = __shfl_up_sync(0xffffffffu, cost, d);
+            const int l = __shfl_up_sync(0xffffffffu, place, d);
+            if (lane >= d) {
+                pre += v;
+                cost += c;
+                place += l;
+            }
         }
-        if (lane == 31) l.total = pre;
+        if (lane == 31) {
+            b.h->n = pre;
+            b.start[pre] = cost;
+            b.first[pre] = (int16_t)place;
+        }
         pre -= mine;
-        int e0 = -1, first = 0, m = 0;
-        if (u >= pre && u < pre + mine) {
-            for (int j = 0; j < per; ++j) {
-                const int e = lane * per + j;
-                const int nb = e < p.E ? (c.cnt[e] + BT - 1) / BT : 0;
-                if (u < pre + nb) {
-                    e0 = e;
-                    first = BT * (u - pre);
-                    m = min(BT, c.cnt[e] - first);
-                    break;
-                }
-                pre += nb;
+        cost -= wt;
+        place -= m;
+        for (int j = 0; j < per; ++j) {
+            const int e = lane * per + j;
+            if (e >= p.E) break;
+            const int c = cnt[e];
+            for (int r = 0; r < c; r += p.bt, ++pre) {
+                b.e[pre] = (int16_t)e;
+                b.first[pre] = (int16_t)(place + r);
+                b.start[pre] = cost;
+                cost += block_weight(min(p.bt, c - r));
             }
+            cnt[e] = place;   // from here on: where the expert's next slot goes
+            place += c;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, e0 >= 0);
-        if (hit != 0) {
-            const int src = __ffs(hit) - 1;
-            e0 = __shfl_sync(0xffffffffu, e0, src);
-            first = __shfl_sync(0xffffffffu, first, src);
-            m = __shfl_sync(0xffffffffu, m, src);
-            int base = -first;
-            for (int i0 = 0; i0 < p.S && base < BT; i0 += 32) {
-                const bool is = i0 + lane < p.S && c.ids[i0 + lane] == e0;
-                const unsigned mask = __ballot_sync(0xffffffffu, is);
-                const int r = base + __popc(mask & lt);
-                if (is && r >= 0 && r < BT) l.slots[0][r] = i0 + lane;
-                base += __popc(mask);
+        __syncwarp();
+        for (int i0 = 0; i0 < p.S; i0 += 32) {   // the slots in ascending order
+            const int i = i0 + lane;
+            int id = i < p.S ? p.ids[i] : -1;
+            if (id >= p.E || id < 0) id = -1;
+            const unsigned same = __match_any_sync(0xffffffffu, id < 0 ? -1 - lane : id);
+            const int at = id < 0 ? 0 : cnt[id] + __popc(same & lt);
+            __syncwarp();
+            if (id >= 0) {
+                b.order[at] = (int16_t)i;
+                if ((same & lt) == 0) cnt[id] = at + __popc(same);
             }
-            if (lane == 0) {
-                l.found[0] = e0;
-                l.found[1] = m;
-            }
+            __syncwarp();
         }
+        share_out(b, units, part, parts);
     }
+    fence_proxy_async_smem();   // cnt lies where the copies will land
     __syncthreads();
-    b.e = l.found[0];
-    b.m = l.found[1];
-    b.nblocks = l.total;
-    return b;
-}
-
-// Code pair j of a word as an MMA operand register (codes j and j + EPS / 2).
-template <int BITS, bool BF>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
-    if constexpr (BITS == 4) {
-        return BF ? and_or(w >> (4 * j), 0x000F000Fu, 0x43004300u) : (w >> (4 * j)) & 0x000F000Fu;
-    } else if constexpr (!BF) {
-        return prmt(w, 0u, j == 0 ? 0x4240u : 0x4341u);
-    } else {
-        const float lo = __uint_as_float(prmt(w, 0x4B000000u, 0x7440u + j)) - 8388608.0f;
-        const float hi = __uint_as_float(prmt(w, 0x4B000000u, 0x7442u + j)) - 8388608.0f;
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
 }
 
 __device__ __forceinline__ float activate(float g, int act) {
@@ -231,371 +315,777 @@ __device__ __forceinline__ float activate(float g, int act) {
     return 0.5f * g * erfcf(-0.70710678118654752f * g);  // gelu
 }
 
-// Ring stages per warp: two CTAs of 8 warps fit an SM and keep 96 KB of words
-// in flight with one token tile (80 KB with two, 64 KB with four, whose rows
-// take twice the shared memory of the words).
-template <int NT> constexpr int stages() { return NT > 2 ? 4 : 5 + (NT == 1); }
-template <int BITS> constexpr int xt_bytes() { return BITS == 4 ? 512 : 256; }  // one token tile of a quad
-template <int BITS, int NT> constexpr int stage_bytes() { return W_BYTES + SZ_BYTES + NT * xt_bytes<BITS>(); }
+// 8 values as 16-bit fixed point with step 2^(E - 141), `inv` = 2^(141 - E): the sum with
+// 1.5 * 2^23 + 128 rounds to an integer whose low 16 bits are x + 128; its second byte is
+// hi, its first, with the top bit flipped, lo: x = 256 hi + lo, both in -128 .. 127.
+// Byte order: 4-bit words, the codes 0 2 4 6 and 1 3 5 7 of a word row; 8-bit, as they come.
+template <int BITS>
+__device__ __forceinline__ void to_fixed(const float (&v)[8], float inv, uint2& hi, uint2& lo) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f + 128.0f));
+    auto four = [&](int a, int b, int c, int d, uint32_t& h, uint32_t& l) {
+        const uint32_t p = prmt(u[a], u[b], 0x5140u), q = prmt(u[c], u[d], 0x5140u);  // bytes a0 b0 a1 b1
+        l = prmt(p, q, 0x5410u) ^ 0x80808080u;
+        h = prmt(p, q, 0x7632u);
+    };
+    if constexpr (BITS == 4) {
+        four(0, 2, 4, 6, hi.x, lo.x);
+        four(1, 3, 5, 7, hi.y, lo.y);
+    } else {
+        four(0, 1, 2, 3, hi.x, lo.x);
+        four(4, 5, 6, 7, hi.y, lo.y);
+    }
+}
 
-// NT: token tiles of 8 MMA columns (UP: 8 slots each, DOWN: 4 slots as hi, lo).
-template <int BITS, bool BF, int NT, bool UP>
-__global__ void __launch_bounds__(MT, NT > 2 ? 1 : 2) moe_kernel(const MoeParams p) {
+// Exponent E of a block whose largest magnitude has the bits `top`: |x| 2^(141 - E) <= 32512 (127 * 256), one more
+// from 1.984 * 2^n up; and its step 2^(E - 141), NaN where a value is not finite.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t top) {
+    return min(max((top + 0x00020000u) >> 23, 15u), 255u);
+}
+__device__ __forceinline__ float block_step(uint32_t top, uint32_t E) {
+    return top >= 0x7F800000u ? NAN : __uint_as_float((E - 14u) << 23);
+}
+
+// Shared memory behind the rings: the warps' partials, the blocks; UP: x's fixed-point values and their steps; DOWN:
+// the sums of y.
+__host__ __device__ constexpr int table_at(int W, int bt) { return W * bt * MCOLS * 4; }
+__host__ __device__ constexpr int values_at(int W, int bt, int S) { return table_at(W, bt) + table_bytes(S); }
+__host__ __device__ constexpr int steps_at(int W, int bt, int S, int xcol) { return values_at(W, bt, S) + 2 * bt * xcol; }
+
+// NT: token tiles of 4 slots (8 MMA columns).  MW: warps, WK of them along K.
+template <int BITS, bool BF, int NT, bool UP, int MW, int WK>
+__global__ void __launch_bounds__(MW * 32, 16 / MW)
+moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_s,
+           const __grid_constant__ CUtensorMap tm_z, const MoeParams p) {
+    constexpr int MT = MW * 32;
     using T16 = Dt<BF>;
-    constexpr bool MBF = UP ? BF : true;        // MMA operand type: x's, or bf16 for h
-    constexpr int EPS = 32 / BITS;
-    constexpr int MMAS = EPS / 4;               // k steps per quad
-    constexpr int TPT = UP ? 8 : 4;             // slots per token tile
-    constexpr int BT = TPT * NT;
-    constexpr int NE = UP ? 2 : 1;              // slots per lane and tile
-    constexpr int ST = stages<NT>();
-    constexpr int SB = stage_bytes<BITS, NT>();
-    constexpr float DSCALE = MBF ? 1.0f : 16777216.0f;              // fp16 operands are q 2^-24
-    constexpr float ZOFF = (MBF && BITS == 4) ? 128.0f : 0.0f;      // bf16 4-bit operands are 128 + q
-    static_assert(BT <= 16 && BT * MCOLS * 4 <= ST * SB, "partials reuse the ring");
-    static_assert(sizeof(Counts) <= MW * ST * SB, "the counts lie in the ring before its first load");
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ Lists lists;
-    __shared__ int last;
+    constexpr int RPS = step_rows<BITS>();       // 4 or 8
+    constexpr int RL = RPS / 4;                  // word rows per lane and step
+    constexpr int SPS = BOX_ROWS / RPS;          // steps per stage
+    constexpr int WC = MW / WK;                  // warps along the columns
+    constexpr int TC = MCOLS * WC;               // weight columns per tile
+    extern __shared__ uint8_t smem_raw[];
+    // the 128-byte swizzle of the TMA boxes repeats every 1024 bytes
+    uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    __shared__ Head head;
+    __shared__ uint64_t bars[MW * NST];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int tile = blockIdx.x;
-    if constexpr (UP) {
-        grid_dependency_wait();   // ids, weights and x may be the previous kernel's output
-        if (blockIdx.y == 0 && tile == 0)
-            for (int i = threadIdx.x; i < p.ntiles_down; i += MT) p.count[i] = 0;
+    // 16-byte column chunk of this lane (columns 4 cg .. 4 cg + 3 of each half): with the lines of a
+    // stage below, the eight lanes of a quarter-warp meet eight different bank groups
+    const int cg = UP ? g : ((g & 1) << 2) | (g >> 1);
+    const int wk = warp / WC, wc = warp % WC;
+    uint64_t* const bar = bars + warp * NST;
+    if (lane == 0) {
+        for (int i = 0; i < NST; ++i) mbar_init(&bar[i], 1);
+        fence_mbarrier_init();
+        if (warp == 1) prefetch_tmap(&tm);
+        if (warp == 2) prefetch_tmap(&tm_s);
+        if (warp == 3) prefetch_tmap(&tm_z);
     }
+    if constexpr (UP) grid_dependency_wait();   // ids, weights and x may be the previous kernel's output
     grid_launch_dependents();
-    const Block b = find_block<BT>(p, blockIdx.y, lists, *reinterpret_cast<Counts*>(smem));
-    if ((int)blockIdx.y >= b.nblocks && !(!UP && blockIdx.y == 0)) return;
-    const int* slots = lists.slots[p.S <= 32 ? warp : 0];
-
-    // ---- this warp's quads
-    const int q0 = min(p.Q, warp * p.QW), nq = b.m > 0 ? min(p.Q, q0 + p.QW) - q0 : 0;
-    const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (ST * SB);
-    // first column of half hf, clamped so that the ragged last tile reads inside the row
-    auto col = [&](int hf, int c) {
-        if constexpr (UP) return hf * p.I + min(tile * 32 + c, p.I - 4);
-        else return min(tile * MCOLS + 32 * hf + c, p.NW - 4);
+    const int Q4 = (p.Q + XBLK - 1) / XBLK;
+    const int rank = UP ? 0 : (int)blockIdx.x % p.cluster;
+    const uint32_t sz_bytes = 256u * (uint32_t)p.sz_rows;   // a stage's s rows, then its z rows
+    const uint32_t roff = MW * NST * (STAGE + sz_bytes);    // behind the rings
+    uint8_t* const tab = smem + roff + table_at(MW, p.bt);
+    const int ts = table_slots(p.S);
+    int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
+    const Blocks blk{&head, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
+    if constexpr (UP) find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), p.ntiles, blockIdx.x, gridDim.x);
+    else find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), Q4, rank, p.cluster);
+    // ---- this CTA's items.  UP: (block, tile) pairs, all steps of K; DOWN: one tile, runs of a block's steps.
+    struct Item {
+        int at, u, tile, s0, ns;   // position on the line, block, column tile, first step, steps
     };
-    const uint32_t* wp[2];
-    const size_t wexp = (size_t)b.e * p.Kw * p.NW, szexp = (size_t)b.e * p.groups * p.NW;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) wp[hf] = p.w + wexp + col(hf, 4 * g);
-    // lane (g, t): t = 0, 1 copies s, z of half 0, t = 2, 3 of half 1
-    const uint16_t* szp = ((t & 1) ? p.z : p.s) + szexp + col(t >> 1, 4 * g);
-    // B operand rows: UP slot g of each tile; DOWN slot g / 2, hi (even g) or lo (odd g)
-    const uint16_t* xp[NT];
-    bool xon[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int pos = n * TPT + (UP ? g : g >> 1);
-        xon[n] = pos < b.m;
-        const int slot = xon[n] ? slots[pos] : 0;
-        if constexpr (UP) xp[n] = p.x + (size_t)(slot / p.top_k) * p.K;
-        else xp[n] = p.h + (size_t)(g & 1) * p.S * p.I + (size_t)slot * p.I;
-        check(slot >= 0 && slot < p.S, &g_moe_status);
-    }
-    auto issue_w = [&](int i) {   // words (and s, z where a group starts) of quad i
-        if (i < nq) {
-            const int q = q0 + i;
-            const uint32_t st = ring + (uint32_t)(i % ST) * SB;
-            const size_t row = (size_t)min(4 * q + t, p.Kw - 1) * p.NW;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-                if (check(b.e < p.E && row + col(hf, 4 * g) + 4 <= (size_t)p.Kw * p.NW, &g_moe_status))
-                    cp_async16(st + 512u * hf + 16u * lane, wp[hf] + row);
-            if (i == 0 || q % p.qpg == 0) {
-                const int grp = q / p.qpg;
-                if (check(grp < p.groups, &g_moe_status))
-                    cp_async8(st + W_BYTES + 64u * t + 8u * g, szp + (size_t)grp * p.NW);
-            }
+    const int end = head.i1;
+    auto open = [&](Item& it) {    // the item at it.at
+        if constexpr (UP) {
+            it.u = it.at / p.ntiles;
+            it.tile = it.at - it.u * p.ntiles;
+            it.s0 = 0;
+            it.ns = p.Q;
+        } else {
+            it.u = it.at / Q4;
+            const int b4 = it.at - it.u * Q4;
+            it.tile = (int)blockIdx.x / p.cluster;
+            it.s0 = b4 * XBLK;
+            it.ns = min(p.Q - it.s0, (end - it.at) * XBLK);
         }
     };
-    auto issue_x = [&](int i) {   // the tokens' values of quad i
-        if (i < nq) {
-            const int r = 4 * (q0 + i) + t;
-            const uint32_t st = ring + (uint32_t)(i % ST) * SB + W_BYTES + SZ_BYTES;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (xon[n] && r < p.Kw) {
-                    if constexpr (BITS == 4) cp_async16(st + 512u * n + 16u * lane, xp[n] + (size_t)r * EPS);
-                    else cp_async8(st + 256u * n + 8u * lane, xp[n] + (size_t)r * EPS);
-                }
-        }
+    auto next = [&](Item& it) { it.at += UP ? 1 : (it.ns + XBLK - 1) / XBLK; };
+    // steps of this warp in an item: [first, first + count), whole fixed-point blocks
+    auto range = [&](const Item& it, int& first) {
+        const int per = ((it.ns + WK - 1) / WK + XBLK - 1) / XBLK * XBLK;
+        first = min(it.ns, wk * per);
+        const int n = min(it.ns, first + per) - first;
+        first += it.s0;
+        return n;
     };
-    // words of the first ST quads before h exists; then their x, one group each
-    for (int i = 0; i < ST; ++i) {
-        issue_w(i);
-        if constexpr (UP) issue_x(i);
-        cp_commit();
-    }
-    if constexpr (!UP) {
-        grid_dependency_wait();
-        for (int i = 0; i < ST; ++i) {
-            issue_x(i);
-            cp_commit();
+    // first column of this warp in a tile (UP: of the gate; the up columns are the map's second plane)
+    auto col = [&](int tile) { return UP ? tile * (TC / 2) + 32 * wc : tile * TC + MCOLS * wc; };
+    // ---- loads: a cursor over the (item, stage) sequence of this warp
+    const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (NST * STAGE);
+    const uint32_t sz_ring = smem_u32(smem) + MW * NST * STAGE + (uint32_t)warp * (NST * sz_bytes);
+    Item wit;
+    wit.at = head.i0;
+    int wq = 0, wleft = 0, wslot = 0;   // next step, stages left in the item, ring slot
+    bool ok = true, wopen = false;
+    auto issue = [&]() {
+        while (wleft == 0) {
+            if (wopen) next(wit);
+            wopen = wit.at < end;
+            if (!wopen) return;
+            open(wit);
+            wleft = (range(wit, wq) + SPS - 1) / SPS;
         }
-    }
-
-    float acc[2][4][NT][NE], d[2][2][NT][4], xs[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) xs[n][k] = 0.0f;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) acc[hf][c][n][e] = 0.0f;
-#pragma unroll
-            for (int T = 0; T < 2; ++T)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) d[hf][T][n][k] = 0.0f;
-        }
-    }
-    const int nt = NT == 1 ? 1 : (b.m + TPT - 1) / TPT;   // tiles that hold slots
-    uint2 sv[2], zv[2];
-    int left = p.qpg - (nq > 0 ? q0 % p.qpg : 0);
-    bool start = true;
-    constexpr uint32_t ONE = MBF ? 0x3F803F80u : 0x3C003C00u;
-    const uint32_t ones[4] = {ONE, ONE, ONE, ONE};
-    for (int i = 0; i < nq; ++i) {
-        cp_wait<ST - 1>();
-        __syncwarp();  // the s and z that other lanes copied
-        const uint32_t st = ring + (uint32_t)(i % ST) * SB;
-        const uint4 wa = lds128_u32(st + 16u * lane), wb = lds128_u32(st + 512u + 16u * lane);
-        if (start) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                sv[hf] = lds64_u32(st + W_BYTES + 128u * hf + 8u * g);
-                zv[hf] = lds64_u32(st + W_BYTES + 128u * hf + 64u + 8u * g);
-            }
-            start = false;
-        }
-        uint32_t bx[NT][EPS / 2];
-        const bool in = 4 * (q0 + i) + t < p.Kw;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t a = st + W_BYTES + SZ_BYTES;
-            if constexpr (BITS == 4) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (xon[n] && in) v = lds128_u32(a + 512u * n + 16u * lane);
-                bx[n][0] = prmt(v.x, v.z, 0x5410u);   // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-                bx[n][1] = prmt(v.x, v.z, 0x7632u);
-                bx[n][2] = prmt(v.y, v.w, 0x5410u);
-                bx[n][3] = prmt(v.y, v.w, 0x7632u);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[wslot], STAGE + sz_bytes);
+            const uint32_t dst = ring + (uint32_t)wslot * STAGE, sz = sz_ring + (uint32_t)wslot * sz_bytes;
+            const int e = blk.e[wit.u], row = e * p.Kw + wq * RPS, grow = e * p.groups + wq / p.spg;
+            const int c = col(wit.tile);
+            if constexpr (UP) {
+                tma_load_3d_u32(dst, &tm, &bar[wslot], c, 0, row);
+                tma_load_3d_u32(sz, &tm_s, &bar[wslot], c, 0, grow);
+                tma_load_3d_u32(sz + sz_bytes / 2, &tm_z, &bar[wslot], c, 0, grow);
             } else {
-                uint2 v = make_uint2(0u, 0u);
-                if (xon[n] && in) v = lds64_u32(a + 256u * n + 8u * lane);
-                bx[n][0] = prmt(v.x, v.y, 0x5410u);   // pairs (0, 2), (1, 3)
-                bx[n][1] = prmt(v.x, v.y, 0x7632u);
+                tma_load_2d_u32(dst, &tm, &bar[wslot], c, row);
+                tma_load_2d_u32(dst + STAGE / 2, &tm, &bar[wslot], c + 32, row);
+                tma_load_2d_u32(sz, &tm_s, &bar[wslot], c, grow);
+                tma_load_2d_u32(sz + sz_bytes / 2, &tm_z, &bar[wslot], c, grow);
             }
         }
-        __syncwarp();  // every lane has read the stage: refill it
-        issue_w(i + ST);
-        issue_x(i + ST);
-        cp_commit();
-        const uint32_t wv[2][4] = {{wa.x, wa.y, wa.z, wa.w}, {wb.x, wb.y, wb.z, wb.w}};
+        wq += SPS;
+        --wleft;
+        wslot ^= 1;
+    };
+    issue();
+    issue();
+
+    if constexpr (!UP) grid_dependency_wait();   // h
+    float* const red = reinterpret_cast<float*>(smem + roff);   // [wk][slot][TC]
+    const uint32_t xoff = roff + values_at(MW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
+    float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));         // UP: [slot][block]
+    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [T][TC]
+    // This lane's 16-byte vectors of word row t (and t + 4): line r of 128 bytes holds them at chunk
+    // cg ^ (r & 7).  UP: the lines of a word row's two halves follow each other; DOWN: 16 lines each.
+    constexpr uint32_t HALF = UP ? 128u : STAGE / 2, LINE = UP ? 256u : 128u;   // to the other half, to the next row
+    auto vec = [&](int r, int hf) {
+        const uint32_t line = UP ? 2 * r + hf : r;
+        return (uint32_t)r * LINE + (uint32_t)hf * HALF + (((uint32_t)cg ^ (line & 7u)) << 4);
+    };
+    // word rows t and t + 4, halves 0 and 1 (UP: rows 4 apart have the same swizzle)
+    const uint32_t off[2][2] = {{vec(t, 0), vec(t, 1)}, {vec(t + 4, 0), vec(t + 4, 1)}};
+    int rslot = 0, phase = 0;   // ring position of the next stage to read
+
+    if constexpr (!UP)
+        for (int i = threadIdx.x; i < p.T * TC; i += MT) ys[i] = 0.0f;   // (a barrier precedes their first use)
+
+    int block = -1;   // UP: the block whose values are in shared memory
+    Item it;
+    for (it.at = head.i0; it.at < end; next(it)) {
+        open(it);
+        int q0;
+        const int nq = range(it, q0);
+        const int16_t* const slots = blk.order + blk.first[it.u];
+        const int bm = blk.count(it.u);
+        if (UP && it.u != block) {
+            // ---- another block: x of its slots as fixed point.  Column 2 m holds hi of the block's slot m, 2 m + 1
+            // its lo: 32 bytes per step, 8 for each word row t.
+            block = it.u;
+            __syncthreads();   // the previous block's values are no longer read
+            // (slot, 8 steps) pairs of this warp, XU at a time so that their loads overlap; a lane has 8 values
+            const int rounds = (nq + 7) / 8, pairs = bm > wc ? (bm - wc + WC - 1) / WC * rounds : 0;
+            constexpr int XU = 4;
+#pragma unroll 1
+            for (int p0 = 0; p0 < pairs; p0 += XU) {
+                uint4 raw[XU];
 #pragma unroll
-        for (int k = 0; k < MMAS; ++k) {
+                for (int u = 0; u < XU; ++u) {
+                    const int pr = min(p0 + u, pairs - 1), m = wc + pr / rounds * WC;
+                    const int q = q0 + pr % rounds * 8 + g, k = q * SK + 8 * t, slot = slots[m];
+                    check(slot >= 0 && slot < p.S, &g_moe_status);
+                    const bool in = q < q0 + nq;
+                    raw[u] = make_uint4(0u, 0u, 0u, 0u);
+                    const uint16_t* const src = p.x + (size_t)(slot / p.top_k) * p.K + k;
+                    if constexpr (BITS == 4) {                // K is a multiple of 8
+                        if (in && k < p.K) raw[u] = *reinterpret_cast<const uint4*>(src);
+                    } else {                                  // K is a multiple of 4
+                        uint2 a = make_uint2(0u, 0u), c = a;
+                        if (in && k < p.K) a = *reinterpret_cast<const uint2*>(src);
+                        if (in && k + 4 < p.K) c = *reinterpret_cast<const uint2*>(src + 4);
+                        raw[u] = make_uint4(a.x, a.y, c.x, c.y);
+                    }
+                }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                if (n < nt) mma_16816<MBF>(xs[n], ones, bx[n][2 * k], bx[n][2 * k + 1]);
+                for (int u = 0; u < XU; ++u) {
+                    if (p0 + u >= pairs) break;
+                    const int pr = p0 + u, m = wc + pr / rounds * WC, qo = pr % rounds * 8 + g, q = q0 + qo;
+                    const bool in = qo < nq;
+                    float v[8];
+                    const uint32_t r0[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = T16::pair(r0[i]);
+                        v[2 * i] = f.x;
+                        v[2 * i + 1] = f.y;
+                    }
+                    uint32_t top = 0;   // bits of the block's largest magnitude, over its 16 lanes
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+                    for (int d = 8; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const uint32_t E = block_exponent(top);
+                    uint2 hi, lo;
+                    to_fixed<BITS>(v, __uint_as_float((268u - E) << 23), hi, lo);
+                    const uint32_t at = xbase + (uint32_t)(2 * m) * p.xcol + (uint32_t)(q - it.s0) * 32u;
+                    if (in && check((q - it.s0) * 32 + 32 <= p.xcol, &g_moe_status)) {
+                        if constexpr (BITS == 4) {
+                            sts64(at + 8u * t, hi.x, hi.y);
+                            sts64(at + p.xcol + 8u * t, lo.x, lo.y);
+                        } else {   // word row j of the step (4 values each): bytes 8 (j % 4) + 4 (j / 4)
+                            const uint32_t j = 2u * t, o = 8u * (j & 3u) + 4u * (j >> 2);
+                            sts32(at + o, hi.x);
+                            sts32(at + o + 8u, hi.y);
+                            sts32(at + p.xcol + o, lo.x);
+                            sts32(at + p.xcol + o + 8u, lo.y);
+                        }
+                    }
+                    if ((lane & 15) == 0 && in && check((q - it.s0) / XBLK < p.nsteps, &g_moe_status))
+                        steps[m * p.nsteps + (q - it.s0) / XBLK] = block_step(top, E);
+                }
+            }
+            __syncthreads();
+        }
+
+        // ---- one item.  AT: token tiles that hold slots of this block
+        auto run = [&](auto at_tag) {
+            constexpr int AT = decltype(at_tag)::value;
+            float acc[2][4][AT];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int T = 0; T < 2; ++T) {
-                    const uint32_t a[4] = {
-                        code_pair<BITS, MBF>(wv[hf][2 * T], 2 * k), code_pair<BITS, MBF>(wv[hf][2 * T + 1], 2 * k),
-                        code_pair<BITS, MBF>(wv[hf][2 * T], 2 * k + 1),
-                        code_pair<BITS, MBF>(wv[hf][2 * T + 1], 2 * k + 1)};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        if (n < nt) mma_16816<MBF>(d[hf][T][n], a, bx[n][2 * k], bx[n][2 * k + 1]);
-                }
-        }
-        if (--left == 0 || i + 1 == nq) {   // the group (or the warp's part of it) ends: fold
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const float2 s01 = T16::pair(sv[hf].x), s23 = T16::pair(sv[hf].y);
-                const float2 z01 = T16::pair(zv[hf].x), z23 = T16::pair(zv[hf].y);
-                const float sc[4] = {s01.x, s01.y, s23.x, s23.y};
-                const float zc[4] = {z01.x + ZOFF, z01.y + ZOFF, z23.x + ZOFF, z23.y + ZOFF};
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < AT; ++n) acc[hf][c][n] = 0.0f;
+            // B column g of token tile n: UP from shared memory; DOWN straight from global memory, a stage ahead (every
+            // CTA reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
+            uint32_t xa[AT], sp[AT];               // UP
+            const int8_t* hp[AT];                  // DOWN: values and steps
+            const float* hs[AT];
+            uint2 bx[SPS][AT];
+            float step_next[2][AT];
+            const int xb = UP ? XBLK : p.hb;       // steps per fixed-point block: XBLK, or 2
 #pragma unroll
-                        for (int e = 0; e < NE; ++e) {
-                            const int k = 2 * (c & 1) + e;
-                            float D = d[hf][c >> 1][n][k], X = xs[n][e];
-                            if constexpr (!UP) {
-                                D += d[hf][c >> 1][n][k + 1];
-                                X += xs[n][1];
-                            }
-                            acc[hf][c][n][e] = fmaf(sc[c], fmaf(D, DSCALE, -zc[c] * X), acc[hf][c][n][e]);
-                        }
-#pragma unroll
-                for (int T = 0; T < 2; ++T)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) d[hf][T][n][k] = 0.0f;
+            for (int n = 0; n < AT; ++n) {
+                if constexpr (UP) {
+                    xa[n] = xoff + (uint32_t)min(8 * n + g, 2 * p.bt - 1) * p.xcol + (uint32_t)(q0 - it.s0) * 32u + 8u * t;
+                    sp[n] = smem_u32(steps + min(4 * n + t, p.bt - 1) * p.nsteps + (q0 - it.s0) / XBLK);
+                } else {
+                    const int col = 2 * slots[min(4 * n + (g >> 1), bm - 1)] + (g & 1);
+                    hp[n] = p.hq + ((size_t)col * p.Qh + q0) * SK + 8 * t;
+                    hs[n] = p.hstep + (size_t)slots[min(4 * n + t, bm - 1)] * p.Qh + q0 / p.hb;
+                    check(col < 2 * p.S, &g_moe_status);
+                }
             }
+            auto request = [&](int i) {            // DOWN: the values of the stage from step i, and its blocks' steps
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < AT; ++n) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) xs[n][k] = 0.0f;
-            left = p.qpg;
-            start = true;
-        }
-    }
-
-    // ---- the warps' partials meet in shared memory: [slot][64], in each warp's own ring
-    cp_wait<0>();
-    __syncwarp();
-    {
-        float* red = reinterpret_cast<float*>(smem + (size_t)warp * (ST * SB));
+                    for (int j = 0; j < SPS; ++j)
+                        if (i + j < nq) bx[j][n] = *reinterpret_cast<const uint2*>(hp[n] + (size_t)(i + j) * SK);
+                    if (i < nq) step_next[0][n] = hs[n][i / xb];
+                    if (SPS == 4 && xb == 2 && i + 2 < nq) step_next[1][n] = hs[n][i / xb + 1];
+                }
+            };
+            if constexpr (!UP) request(0);
+            int d[2][2][AT][4], xs[AT][4];
+            // The sums start at the bits of 1.5 * 2^23: an integer of at most 22 bits added to them is, read
+            // as a float, that much more (128 * 255 * 128 < 2^22), so no conversion is needed.
+            constexpr int BIAS = 0x4B400000;
+            auto sum_value = [](int hi, int lo) {
+                return fmaf(256.0f, __int_as_float(hi) - 12582912.0f, __int_as_float(lo) - 12582912.0f);
+            };
+            auto clear = [&]() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < AT; ++n)
 #pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                const int pos = n * TPT + (UP ? 2 * t + e : t);
-                if (pos < b.m)
+                    for (int k = 0; k < 4; ++k) {
+                        xs[n][k] = BIAS;
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) d[hf][0][n][k] = d[hf][1][n][k] = BIAS;
+                    }
+            };
+            // step i of the warp's range, at step j of the stage
+            // (st: the stage, xi: this lane's x values in it; plain loads, whose constant offsets fold)
+            // first: a new sum, from BIAS
+            auto mult = [&](bool first, const uint8_t* st, const uint8_t* const (&xi)[AT], int j) {
+                uint2 b[AT];
+#pragma unroll
+                for (int n = 0; n < AT; ++n) b[n] = UP ? *reinterpret_cast<const uint2*>(xi[n] + 32 * j) : bx[j][n];
+                uint4 w[RL][2];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int r = 0; r < RL; ++r) {   // rows 4 j + t (4-bit), 8 j + t and 8 j + t + 4 (8-bit)
+                        const int row8 = BITS == 4 ? j >> 1 : j, odd = BITS == 4 ? j & 1 : r;
+                        w[r][hf] = *reinterpret_cast<const uint4*>(st + off[odd][hf] + 8 * LINE * row8);
+                    }
+#pragma unroll
+                for (int n = 0; n < AT; ++n)
+                    mma_u8s8(first, xs[n], 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b[n], BIAS);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t a[2][4];   // k 0-15 and 16-31 of the lane's four columns
+                    const uint32_t v0[4] = {w[0][hf].x, w[0][hf].y, w[0][hf].z, w[0][hf].w};
+                    if constexpr (BITS == 4) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            a[0][c] = v0[c] & 0x0F0F0F0Fu;
+                            a[1][c] = (v0[c] >> 4) & 0x0F0F0F0Fu;
+                        }
+                    } else {
+                        const uint32_t v1[4] = {w[RL - 1][hf].x, w[RL - 1][hf].y, w[RL - 1][hf].z, w[RL - 1][hf].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            a[0][c] = v0[c];
+                            a[1][c] = v1[c];
+                        }
+                    }
+#pragma unroll
+                    for (int T = 0; T < 2; ++T)
+#pragma unroll
+                        for (int n = 0; n < AT; ++n)
+                            mma_u8s8(first, d[hf][T][n], a[0][2 * T], a[0][2 * T + 1], a[1][2 * T], a[1][2 * T + 1], b[n],
+                                        BIAS);
+                }
+            };
+            // the block (or the group) ends: acc += s step (D - z X)
+            auto fold = [&](int i, int k, uint32_t sz) {   // k: the block's place in the stage; sz: the group's s row in it
+                float step[AT], X[AT];
+#pragma unroll
+                for (int n = 0; n < AT; ++n) {
+                    step[n] = UP ? __uint_as_float(lds32_u32(sp[n] + 4u * (i / XBLK))) : step_next[k][n];
+                    X[n] = sum_value(xs[n][0], xs[n][1]);
+                }
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint2 sv = lds64_u32(sz + 64u * hf), zv = lds64_u32(sz + 64u * hf + sz_bytes / 2);
+                    const float2 s01 = T16::pair(sv.x), s23 = T16::pair(sv.y);
+                    const float2 z01 = T16::pair(zv.x), z23 = T16::pair(zv.y);
+                    const float sc[4] = {s01.x, s01.y, s23.x, s23.y};
+                    const float zc[4] = {z01.x, z01.y, z23.x, z23.y};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int n = 0; n < AT; ++n) {
+                            const int k = 2 * (c & 1);
+                            const float D = sum_value(d[hf][c >> 1][n][k], d[hf][c >> 1][n][k + 1]);
+                            // (s step first: the other product can pass fp32's range where the result does not)
+                            acc[hf][c][n] = fmaf(sc[c] * step[n], fmaf(-zc[c], X[n], D), acc[hf][c][n]);
+                        }
+                }
+            };
+            int gleft = p.spg - q0 % p.spg;   // steps left in the current group
+            bool fresh = false;               // the next step starts a group
+#pragma unroll 1
+            for (int i = 0; i < nq; i += SPS) {
+                if (ok) {
+                    const bool good = mbar_wait_bounded(&bar[rslot], (uint32_t)phase, WAIT_NS);
+                    if (!good) atomicOr(&g_moe_status, 1u);
+                    ok = __all_sync(0xffffffffu, good);
+                }
+                if (!ok) break;
+                const uint8_t* const st = smem + (uint32_t)(warp * NST + rslot) * STAGE;
+                uint32_t sz = sz_ring + (uint32_t)rslot * sz_bytes + 8u * cg;   // the stage's first group
+                const uint8_t* xi[AT];
+#pragma unroll
+                for (int n = 0; n < AT; ++n) xi[n] = UP ? smem + xa[n] + 32u * i : nullptr;
+                // D starts anew with each fixed-point block (xb steps from the start of the range) and each group
+                if (i + SPS <= nq && gleft >= SPS && SPS <= xb) {   // a whole stage inside one group and block
+                    if constexpr (SPS == XBLK) {
+                        mult(true, st, xi, 0);
+                    } else {
+                        if (i % xb == 0 || fresh) clear();
+                        mult(false, st, xi, 0);
+                    }
+                    fresh = false;
+#pragma unroll
+                    for (int j = 1; j < SPS; ++j) mult(false, st, xi, j);
+                    gleft -= SPS;
+                    if (SPS == XBLK || (i + SPS) % xb == 0 || gleft == 0 || i + SPS >= nq) fold(i, 0, sz);
+                    if (gleft == 0) {
+                        gleft = p.spg;
+                        fresh = true;
+                    }
+                } else {                               // short groups, or the range's end: step by step
+#pragma unroll
+                    for (int j = 0; j < SPS; ++j) {
+                        if (i + j >= nq) break;
+                        if ((i + j) % xb == 0 || fresh) clear();
+                        fresh = false;
+                        mult(false, st, xi, j);
+                        if (--gleft == 0 || (i + j + 1) % xb == 0 || i + j + 1 == nq) fold(i + j, SPS == 4 && xb == 2 ? j / 2 : 0, sz);
+                        if (gleft == 0) {
+                            gleft = p.spg;
+                            fresh = true;
+                            sz += 128u;
+                        }
+                    }
+                }
+                if constexpr (!UP) request(i + SPS);
+                __syncwarp();   // every lane has read the stage: refill it
+                fence_proxy_async_smem();
+                issue();
+                rslot ^= 1;
+                phase ^= rslot == 0;
+            }
+            // ---- the warps' partials meet in shared memory
+#pragma unroll
+            for (int n = 0; n < AT; ++n) {
+                const int pos = 4 * n + t;
+                if (pos < bm)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
-                        *reinterpret_cast<float4*>(red + pos * MCOLS + 32 * hf + 4 * g) =
-                            make_float4(acc[hf][0][n][e], acc[hf][1][n][e], acc[hf][2][n][e], acc[hf][3][n][e]);
+                        *reinterpret_cast<float4*>(red + (wk * p.bt + pos) * TC + MCOLS * wc + 32 * hf + 4 * cg) =
+                            make_float4(acc[hf][0][n], acc[hf][1][n], acc[hf][2][n], acc[hf][3][n]);
             }
-    }
-    __syncthreads();
-    auto total = [&](int i) {   // over the warps, in their order
-        float v = 0.0f;
+        };
+        if (NT == 1 || bm <= 4) run(std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, NT>{});
+        __syncthreads();
+        if constexpr (UP) {
+            // The tile's TC / 2 values of h of one slot are one fixed-point block (128 or 64): LPS lanes, 4 each
+            constexpr int LPS = TC / 8, SPW = 32 / LPS;
+            const int c = 4 * (lane % LPS), cc = it.tile * (TC / 2) + c;
+            for (int pos0 = warp * SPW; pos0 < bm; pos0 += MW * SPW) {
+                const int pos = min(pos0 + lane / LPS, bm - 1);
+                const bool mine = pos0 + lane / LPS < bm;
+                const float* const src = red + pos * TC + MCOLS * (c / 32) + c % 32;   // gate; its up column 32 on
+                float4 ga = make_float4(0.0f, 0.0f, 0.0f, 0.0f), ua = ga;
 #pragma unroll
-        for (int w = 0; w < MW; ++w) v += reinterpret_cast<const float*>(smem + (size_t)w * (ST * SB))[i];
-        return v;
-    };
-    if constexpr (UP) {
-        for (int i = threadIdx.x; i < b.m * 32; i += MT) {
-            const int pos = i >> 5, c = i & 31, cc = tile * 32 + c;
-            if (cc >= p.I) continue;
-            const float v = activate(total(pos * MCOLS + c), p.act) * total(pos * MCOLS + 32 + c);
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
-            uint16_t* dst = p.h + (size_t)slots[pos] * p.I + cc;
-            dst[0] = __bfloat16_as_ushort(hi);
-            dst[(size_t)p.S * p.I] = __bfloat16_as_ushort(lo);
+                for (int w = 0; w < WK; ++w) {   // over the warps along K, in their order
+                    const float4 a = *reinterpret_cast<const float4*>(src + w * p.bt * TC);
+                    const float4 b = *reinterpret_cast<const float4*>(src + w * p.bt * TC + 32);
+                    ga.x += a.x; ga.y += a.y; ga.z += a.z; ga.w += a.w;
+                    ua.x += b.x; ua.y += b.y; ua.z += b.z; ua.w += b.w;
+                }
+                const float gv[4] = {ga.x, ga.y, ga.z, ga.w}, uv[4] = {ua.x, ua.y, ua.z, ua.w};
+                float v[8] = {};
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (cc < p.I) v[i] = activate(gv[i], p.act) * uv[i];   // I is a multiple of 4
+                    top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+                }
+#pragma unroll
+                for (int d = LPS / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const uint32_t E = block_exponent(top);
+                uint2 hi, lo;
+                to_fixed<8>(v, __uint_as_float((268u - E) << 23), hi, lo);   // bytes 0 1 2 3 in .x
+                const int slot = slots[pos], q = cc / SK;
+                int8_t* const row = p.hq + ((size_t)(2 * slot) * p.Qh + q) * SK;   // lo: Qh * SK bytes on
+                const bool in = mine && q < p.Qh && check(slot >= 0 && slot < p.S, &g_moe_status);
+                if constexpr (BITS == 4) {
+                    // a word row's 8 values are two lanes': the even one stores hi, the odd one lo, as 0 2 4 6 1 3 5 7
+                    const bool odd = lane & 1;
+                    const uint32_t give = odd ? hi.x : lo.x, keep = odd ? lo.x : hi.x;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
+                    const uint32_t a = odd ? got : keep, b = odd ? keep : got;   // values 0-3 and 4-7
+                    if (in)
+                        *reinterpret_cast<uint2*>(row + (odd ? (size_t)p.Qh * SK : 0) + 8 * (c % SK / 8)) =
+                            make_uint2(prmt(a, b, 0x6420u), prmt(a, b, 0x7531u));
+                } else if (in) {   // word row j of the step: bytes 8 (j % 4) + 4 (j / 4)
+                    const int j = c % SK / 4, o = 8 * (j & 3) + 4 * (j >> 2);
+                    *reinterpret_cast<uint32_t*>(row + o) = hi.x;
+                    *reinterpret_cast<uint32_t*>(row + (size_t)p.Qh * SK + o) = lo.x;
+                }
+                if (in && lane % LPS == 0) p.hstep[(size_t)slot * p.Qh + q / (TC / 2 / SK)] = block_step(top, E);
+            }
+            __syncthreads();   // the partials are read: the next item may write its own
+        } else {
+            // y += weight * row: a thread takes one column of the tokens t = its group mod MT / TC, so two slots
+            // of one token meet in one thread
+            const int c = threadIdx.x % TC, grp = threadIdx.x / TC;
+            auto total = [&](int o) {   // over the warps along K, in their order
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WK; ++w) v += red[w * p.bt * TC + o];
+                return v;
+            };
+            for (int pos = 0; pos < bm; ++pos) {
+                const int sl = slots[pos], tok = sl / p.top_k;
+                if (tok % (MT / TC) == grp) ys[tok * TC + c] = fmaf(p.weights[sl], total(pos * TC + c), ys[tok * TC + c]);
+            }
+            __syncthreads();   // the partials are read: the next item may write its own
         }
-    } else {
-        for (int i = threadIdx.x; i < b.m * MCOLS; i += MT) {
-            const int pos = i / MCOLS, cc = tile * MCOLS + i % MCOLS;
-            if (cc < p.NW) p.part[(size_t)slots[pos] * p.NW + cc] = total(i);
+    }
+    if (!ok)   // gave up a wait: give the copies still in flight as long again
+        for (int i = 0; i < NST; ++i) {
+            mbar_wait_bounded(&bar[rslot], (uint32_t)phase, WAIT_NS);
+            rslot ^= 1;
+            phase ^= rslot == 0;
         }
-        // the last of the tile's blocks to arrive sums the slots of each token
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            last = b.nblocks == 0 || atomicAdd(&p.count[tile], 1u) == (unsigned)b.nblocks - 1u;
-        __syncthreads();
-        if (!last) return;
-        __threadfence();
-        for (int i = threadIdx.x; i < p.T * (MCOLS / 4); i += MT) {
-            const int tok = i / (MCOLS / 4), cc = tile * MCOLS + 4 * (i % (MCOLS / 4));
+    if constexpr (!UP) {
+        // ---- the tile's CTAs join their sums, in their order; each writes its share of the rows
+        if (p.cluster > 1) cluster_sync();
+        else __syncthreads();
+        const int tl = (int)blockIdx.x / p.cluster;
+        const uint32_t at = smem_u32(ys);
+        for (int i = rank + p.cluster * (int)threadIdx.x; i < p.T * (TC / 4); i += p.cluster * MT) {
+            const int tok = i / (TC / 4), cc = tl * TC + 4 * (i % (TC / 4));
             if (cc >= p.NW) continue;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int j = 0; j < p.top_k; ++j) {
-                const int slot = tok * p.top_k + j, id = p.ids[slot];
-                if (id < 0 || id >= p.E) continue;
-                const float a = p.weights[slot];
-                const float4 r = __ldcg(reinterpret_cast<const float4*>(p.part + (size_t)slot * p.NW + cc));
-                v.x = fmaf(a, r.x, v.x);
-                v.y = fmaf(a, r.y, v.y);
-                v.z = fmaf(a, r.z, v.z);
-                v.w = fmaf(a, r.w, v.w);
+            if (p.cluster == 1) {
+                v = *reinterpret_cast<const float4*>(ys + 4 * i);
+            } else {
+                for (int r = 0; r < p.cluster; ++r) {
+                    const float4 o = ld_cluster_f4(map_shared_rank(at + 16u * i, r));
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
             }
             uint2 o;
             o.x = (uint32_t)T16::store(v.x) | ((uint32_t)T16::store(v.y) << 16);
             o.y = (uint32_t)T16::store(v.z) | ((uint32_t)T16::store(v.w) << 16);
             *reinterpret_cast<uint2*>(p.y + (size_t)tok * p.NW + cc) = o;
         }
+        __syncwarp();
+        if (p.cluster > 1) cluster_sync();   // peers keep their shared memory until every read is done
     }
 }
 
-template <int BITS, bool BF, int NT, bool UP>
-wq_status launch_one(const MoeParams& p, int tiles, bool pdl, cudaStream_t stream) {
-    auto kern = moe_kernel<BITS, BF, NT, UP>;
-    static std::atomic<uint64_t> attr_ctx[MAX_DEVICES];
-    constexpr int smem = MW * stages<NT>() * stage_bytes<BITS, NT>();
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
-    if (const wq_status st = ensure_smem_attr((const void*)kern, smem, attr_ctx, dev); st != WQ_OK) return st;
-    constexpr int BT = (UP ? 8 : 4) * NT;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tiles, std::min(p.S, std::min(p.E, p.S) + p.S / BT), 1);
-    cfg.blockDim = dim3(MT, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return from_cuda(cudaLaunchKernelEx(&cfg, kern, p));
+// Dynamic shared memory a CTA of 16 warps (one per SM) or 8 (two) can have.
+constexpr int max_smem(int W) { return W == 16 ? 225 * 1024 : 112 * 1024; }
+constexpr int ring_bytes(int W, int sz_rows) { return 1024 + W * NST * (STAGE + 256 * sz_rows); }
+// s rows of the groups that a stage of `sps` steps, starting at a multiple of them, can touch.
+int stage_groups(int spg, int sps) { return spg % sps == 0 ? 1 : std::min(sps, (sps - 1) / spg + 2); }
+
+int xcol_bytes(int steps) {   // 32 mod 128: the four columns of a load phase lie in different banks
+    const int b = steps * 32;
+    return b + (160 - b % 128) % 128;
+}
+// How a product of inner length K is cut.
+struct Cut {
+    int spg, sz_rows;     // steps per group, s rows per stage
+    int bt;               // slots per block
+    int W, WK, cluster;   // warps, warps along K, CTAs per column tile (DOWN)
+    int xcol, nsteps, smem;
+};
+int warp_steps(int QC, int WK) { return ((QC + WK - 1) / WK + XBLK - 1) / XBLK * XBLK; }
+
+void cut_smem(Cut& c, bool up, int T, int S, int Q) {
+    c.xcol = up ? xcol_bytes(Q) : 0;
+    c.nsteps = up ? (Q + XBLK - 1) / XBLK : 0;
+    c.smem = ring_bytes(c.W, c.sz_rows) + (up ? steps_at(c.W, c.bt, S, c.xcol) + c.bt * c.nsteps * 4
+                                              : values_at(c.W, c.bt, S) + T * MCOLS * (c.W / c.WK) * 4);
 }
 
-void set_product(MoeParams& p, int K, int G, int eps) {
+// UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
+// leave room for (bt = 0: K is too long).  Few tokens and tiles: CTAs of 8 warps, beside which DOWN's find room
+// while they run; else of 16, 4 of them along K or 8, what leaves fewer steps idle.
+Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
+    const int Q = (K + SK - 1) / SK;
+    Cut c{};
+    c.spg = group_size == -1 || group_size == K ? 1 << 29 : group_size / SK;
+    c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
+    c.cluster = 1;
+    if (T <= 4 && (long long)((I + 63) / 64) * std::min(S, E) <= FEW_TILES) {
+        c.W = 8;
+        c.WK = 4;
+        c.bt = 4;
+        cut_smem(c, true, T, S, Q);
+        if (c.smem <= max_smem(8)) return c;
+    }
+    c.W = 16;
+    c.WK = 8 * warp_steps(Q, 8) < 4 * warp_steps(Q, 4) ? 8 : 4;
+    for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; --c.bt) {
+        cut_smem(c, true, T, S, Q);
+        if (c.smem <= max_smem(16)) break;
+    }
+    return c;
+}
+
+// Clusters of cs CTAs of 8 warps, two per SM, that the device holds at once (a GPC's SMs are not a multiple of
+// every size: 15 clusters of 8 with one CTA per SM on a B200, not 148 / 8 = 18).  Asked once per device.
+int clusters_that_fit(int cs) {
+    static std::atomic<int> known[MAX_DEVICES][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 2 * sm_count() / cs;
+    int n = known[dev][cs].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    n = 2 * sm_count() / cs;
+    if (cs > 1) {
+        auto kern = moe_kernel<4, false, 1, false, 8, 8>;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(cs, 1, 1);
+        cfg.blockDim = dim3(256, 1, 1);
+        cfg.dynamicSmemBytes = max_smem(8);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = cs;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int found = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem(8)) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&found, kern, &cfg) == cudaSuccess && found > 0)
+            n = found;
+        else
+            cudaGetLastError();
+    }
+    known[dev][cs].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// DOWN: CTAs of 8 warps.  A column tile is worked on by a cluster, of the size (and with the width of tile) that
+// leaves the fewest places of the SMs without a CTA: two per SM, so that one streams while the other ends an item,
+// or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit an empty
+// device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
+Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
+    const int places = few ? sm_count() : 2 * sm_count();
+    Cut c{};
+    c.W = 8;
+    c.spg = group_size == -1 || group_size == I ? 1 << 29 : group_size / SK;
+    c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
+    int best = -1;   // places taken, in percent
+    for (const int WK : {8, 4}) {
+        const int tiles = (N + MCOLS * c.W / WK - 1) / (MCOLS * c.W / WK);
+        for (int cs = 1; cs <= 8; ++cs) {
+            const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
+            const int fit = std::max(1, few ? all / 2 : all);
+            const int waves = (tiles + fit - 1) / fit, use = (int)(100ll * tiles * cs / ((long long)waves * places));
+            if (use > best + 2 || (few && use >= best && WK == 4)) {
+                best = use;
+                c.WK = WK;
+                c.cluster = cs;
+            }
+        }
+    }
+    // (many tokens and small groups: narrow tiles, then blocks of fewer slots; 2 always fit)
+    for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; c.bt /= 2) {
+        cut_smem(c, false, T, S, 0);
+        if (c.smem > max_smem(8)) {
+            c.WK = 8;
+            cut_smem(c, false, T, S, 0);
+        }
+        if (c.smem <= max_smem(8)) break;
+    }
+    return c;
+}
+
+template <int BITS, bool BF, int NT, bool UP, int W, int WK>
+wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, bool pdl, cudaStream_t stream) {
+    auto kern = moe_kernel<BITS, BF, NT, UP, W, WK>;
+    static std::atomic<uint64_t> attr_ctx[MAX_DEVICES];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
+    if (const wq_status st = ensure_smem_attr((const void*)kern, max_smem(W), attr_ctx, dev); st != WQ_OK) return st;
+    // More blocks than these cannot be: each expert's last block may be short.
+    const int blocks = std::min(p.S, std::min(p.E, p.S) + p.S / p.bt);
+    if ((long long)blocks * 5 * std::max(p.ntiles, (p.Q + XBLK - 1) / XBLK) >= 1ll << 31) return WQ_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    const long long ctas = UP ? std::min<long long>(sm_count() * (16 / W), (long long)blocks * p.ntiles)
+                              : (long long)p.ntiles * p.cluster;
+    if (ctas > 0x7fffffffll) return WQ_ERR_UNSUPPORTED;
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(W * 32, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    int na = 0;
+    if (!UP && p.cluster > 1) {
+        attrs[na].id = cudaLaunchAttributeClusterDimension;
+        attrs[na].val.clusterDim.x = p.cluster;
+        attrs[na].val.clusterDim.y = 1;
+        attrs[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (pdl) {
+        attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = attrs;
+    cfg.numAttrs = na;
+    return from_cuda(cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], p));
+}
+
+// One product: its shape, its launch.
+template <int BITS, bool BF, bool UP>
+wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const uint16_t* z, int K, int group_size,
+                      const Cut& c, bool pdl, cudaStream_t stream) {
     p.K = K;
-    p.Kw = K / eps;
-    p.Q = (p.Kw + 3) / 4;
-    p.QW = (p.Q + MW - 1) / MW;
-    p.qpg = G == K ? (1 << 29) : G / (4 * eps);
-    p.groups = G == K ? 1 : K / G;
+    p.Kw = K * BITS / 32;
+    p.Q = (K + SK - 1) / SK;
+    p.bt = c.bt; p.spg = c.spg; p.sz_rows = c.sz_rows;
+    p.cluster = c.cluster; p.xcol = c.xcol; p.nsteps = c.nsteps;
+    p.groups = group_size == -1 ? 1 : K / group_size;
+    // UP: planes of I columns, gate and up; DOWN: rows of N columns (words in boxes of 32, s and z of 64)
+    CUtensorMap tm[3];
+    const uint64_t cols = UP ? p.I : p.NW, planes = UP ? 2 : 1, wrows = (uint64_t)p.E * p.Kw;
+    const uint64_t srows = (uint64_t)p.E * p.groups;
+    const uint32_t sc = UP ? 32 : 64, bp = UP ? 2 : 1;
+    const int dims = UP ? 3 : 2;
+    if (!make_map_rows(&tm[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, w, 4, dims, cols, planes, wrows, 32, bp, BOX_ROWS,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_rows(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, s, 2, dims, cols, planes, srows, sc, bp, p.sz_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map_rows(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, z, 2, dims, cols, planes, srows, sc, bp, p.sz_rows,
+                       CU_TENSOR_MAP_SWIZZLE_NONE))
+        return WQ_ERR_CUDA;
+    const int warp_tiles = UP ? (p.I + 31) / 32 : (p.NW + MCOLS - 1) / MCOLS;   // of 64 columns
+    auto go = [&](auto nt, auto w, auto wk) {
+        constexpr int NT = decltype(nt)::value, W = decltype(w)::value, WK = decltype(wk)::value;
+        p.ntiles = (warp_tiles + W / WK - 1) / (W / WK);
+        return launch_one<BITS, BF, NT, UP, W, WK>(tm, p, c.smem, pdl, stream);
+    };
+    using N1 = std::integral_constant<int, 1>;
+    using N2 = std::integral_constant<int, 2>;
+    using N4 = std::integral_constant<int, 4>;
+    using N8 = std::integral_constant<int, 8>;
+    using N16 = std::integral_constant<int, 16>;
+    if constexpr (UP) {
+        if (c.W == 8) return go(N1{}, N8{}, N4{});
+        if (c.bt <= 4) return c.WK == 4 ? go(N1{}, N16{}, N4{}) : go(N1{}, N16{}, N8{});
+        return c.WK == 4 ? go(N2{}, N16{}, N4{}) : go(N2{}, N16{}, N8{});
+    } else {
+        if (c.bt <= 4) return c.WK == 4 ? go(N1{}, N8{}, N4{}) : go(N1{}, N8{}, N8{});
+        return c.WK == 4 ? go(N2{}, N8{}, N4{}) : go(N2{}, N8{}, N8{});
+    }
 }
 
 template <int BITS, bool BF>
 wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
-    constexpr int EPS = 32 / BITS;
     MoeParams p{};
     p.x = m.x; p.ids = m.ids; p.weights = m.weights; p.y = m.y;
     p.T = m.T; p.top_k = m.top_k; p.S = m.T * m.top_k; p.E = m.E; p.I = m.I; p.act = m.act;
-    p.ntiles_down = (m.N + MCOLS - 1) / MCOLS;
-    uint8_t* ws = static_cast<uint8_t*>(m.ws);
-    const MoeLayout lay = moe_layout(m.T, m.top_k, m.I, m.N);
-    p.count = reinterpret_cast<unsigned int*>(ws);
-    p.h = reinterpret_cast<uint16_t*>(ws + lay.off_h);
-    p.part = reinterpret_cast<float*>(ws + lay.off_part);
-
-    p.w = m.w_up; p.s = m.s_up; p.z = m.z_up;
-    p.NW = 2 * m.I; p.NC = m.I;
-    set_product(p, m.K, m.group_size == -1 ? m.K : m.group_size, EPS);
-    const bool pdl = (m.flags & WQ_FLAG_PDL) != 0;
-    const int up_tiles = (m.I + 31) / 32;
-    wq_status st = m.T <= 8 ? launch_one<BITS, BF, 1, true>(p, up_tiles, pdl, stream)
-                            : launch_one<BITS, BF, 2, true>(p, up_tiles, pdl, stream);
+    const Cut up = cut_up(m.T, p.S, p.E, m.K, m.I, m.group_size, BITS);
+    p.Qh = (m.I + SK - 1) / SK;
+    p.hb = MCOLS * (up.W / up.WK) / 2 / SK;   // a tile of UP: 128 values or 64
+    const Cut down = cut_down(m.T, p.S, m.I, m.N, m.group_size, BITS, up.W == 8);
+    if (up.bt == 0 || down.bt == 0) return WQ_ERR_UNSUPPORTED;
+    p.hq = static_cast<int8_t*>(m.ws);
+    p.hstep = reinterpret_cast<float*>(p.hq + (size_t)2 * p.S * p.Qh * SK);
+    p.NW = 2 * m.I;
+    const wq_status st = run_product<BITS, BF, true>(p, m.w_up, m.s_up, m.z_up, m.K, m.group_size, up,
+                                                     (m.flags & WQ_FLAG_PDL) != 0, stream);
     if (st != WQ_OK) return st;
-
-    p.w = m.w_down; p.s = m.s_down; p.z = m.z_down;
-    p.NW = p.NC = m.N;
-    set_product(p, m.I, m.group_size == -1 ? m.I : m.group_size, EPS);
-    if (m.T <= 4) return launch_one<BITS, BF, 1, false>(p, p.ntiles_down, true, stream);
-    if (m.T <= 8) return launch_one<BITS, BF, 2, false>(p, p.ntiles_down, true, stream);
-    return launch_one<BITS, BF, 4, false>(p, p.ntiles_down, true, stream);
+    p.NW = m.N;
+    return run_product<BITS, BF, false>(p, m.w_down, m.s_down, m.z_down, m.I, m.group_size, down, true, stream);
 }
 
 }  // namespace
 
-// Workspace: arrival counters, h (two bf16 planes), the fp32 rows per slot.
-MoeLayout moe_layout(int T, int top_k, int I, int N) {
-    const size_t S = (size_t)T * top_k;
-    auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-    MoeLayout l;
-    l.off_h = up((size_t)((N + MCOLS - 1) / MCOLS) * 4);
-    l.off_part = l.off_h + up(S * I * 4);
-    l.bytes = l.off_part + up(S * N * 4);
-    return l;
+// Workspace: h's two bytes per value, then its steps (at most one per step of K).
+size_t moe_workspace_bytes(int T, int top_k, int I) {
+    const size_t rows = (size_t)T * top_k * ((I + SK - 1) / SK);
+    return (rows * (2 * SK + 4) + 255) & ~(size_t)255;
 }
 
 wq_status launch_moe(const MoeProblem& m, cudaStream_t stream) {
@@ -611,7 +1101,7 @@ wq_status moe_device_status(int reset) {
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(g_moe_status, &zero, sizeof(zero)) != cudaSuccess) return WQ_ERR_CUDA;
     }
-    return (v & 2u) ? WQ_ERR_CHECK : WQ_OK;
+    return (v & 1u) ? WQ_ERR_TIMEOUT : (v & 2u) ? WQ_ERR_CHECK : WQ_OK;
 }
 
 }  // namespace wq

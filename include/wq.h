@@ -413,19 +413,23 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  *   activation  WQ_ACT_SILU: g / (1 + exp(-g)); WQ_ACT_GELU: g * Phi(g), the exact form.
  *   workspace   wq_moe_workspace_size() bytes of device memory, 256-byte aligned,
  *            any contents; calls that may run at the same time must not share it.
- * Sums are fp32; h is kept as a pair of bfloat16 (16 significant bits, fp32's
- * range); y is rounded once.  The result does not depend on timing: slots are
- * summed in order.  Values of x have to be finite (else the rows that hold
- * others become NaN or infinite; no other row does).
+ * The codes are multiplied as integers: x and h (fp32) become 16-bit fixed
+ * point, with a power-of-two step per token and aligned block of 128 values
+ * that puts the block's largest between 2^14 and 2^15 (error at most 2^-15 of
+ * that value; none for values that end at or above the step).  Their products
+ * are summed exactly over a block, blocks and slots in fp32, in an order that
+ * does not depend on timing; y is rounded once.  A row of x that holds NaN or an
+ * infinity becomes NaN; no other row does.
  * bits 4 or 8 (else WQ_ERR_UNSUPPORTED).  1 <= T <= WQ_MOE_MAX_TOKENS,
- * 1 <= top_k <= 16, 1 <= E <= WQ_MOE_MAX_EXPERTS.  K and inner multiples of eps
- * and of the group size (-1: one group per column), the group size a multiple
- * of 4 * eps as for wq_gemv; inner and N multiples of 8.  Arrays of 16-bit
+ * 1 <= top_k <= 16, 1 <= E <= WQ_MOE_MAX_EXPERTS, K <= WQ_MOE_MAX_K.  K and
+ * inner multiples of eps and of the group size (-1: one group per column), the
+ * group size a multiple of 32 (else WQ_ERR_UNSUPPORTED); inner and N multiples of 8.  Arrays of 16-bit
  * values and words 16-byte aligned, ids and weights 4-byte.  flags:
  * WQ_FLAG_BF16, WQ_FLAG_PDL (all inputs are read after the previous kernel on
  * the stream has completed).
  */
 #define WQ_MOE_MAX_TOKENS 64
+#define WQ_MOE_MAX_K 24576
 #define WQ_MOE_MAX_SLOTS (WQ_MOE_MAX_TOKENS * 16)
 #define WQ_ACT_SILU 0
 #define WQ_ACT_GELU 1

@@ -1,17 +1,17 @@
 """A mixture-of-experts layer in 64 bits from the definition, with a bound of the
-fp32 / bf16 arithmetic that the kernels are allowed.
+fixed-point and fp32 arithmetic that the kernels are allowed.
 
-Error terms, u = 2^-24 (half a step of fp32), with w' = |x| (128 + q + |z|) s the
-magnitude a product is summed at (bf16 4-bit codes are 128 + q):
-  * a group's sums D and X: one addition per 16 values in the matrix unit, at most
-    2u each (it may truncate), so (G / 16 + 2) 2u sum(w') over the group;
-  * the fold (three roundings per group), the 8 warps and the activation's argument:
-    (3 + groups + 8) u of the same magnitude;
-  * h: |act'| <= 1.13 for both activations; exp, erfc, the division and the product
-    a few u (taken as 16 u); h = hi + lo in bf16 rounds once at 2^-18 relative;
-  * DOWN sums the same way over h, then the slots (top_k + 2 roundings);
-  * y rounds once: half a step of its type, relative to the value (and half the
-    smallest subnormal step).
+Error terms, u = 2^-24 (half a step of fp32):
+  * x, and h, are held in fixed point: at most 1.02 * 2^-15 of the largest magnitude of
+    their block of 128, for each value;
+  * a block's integer sums are exact; with w' = |x| (q + |z|) s the magnitude that it is
+    folded at, the conversion, the zero point, the step and s round 5 times, the additions
+    of up to K / 32 folds and 8 warps once each: (13 + K / 32) u sum(w');
+  * h: |act'| <= 1.13 for both activations; exp, erfc, the division and the product a few
+    u (taken as 16 u);
+  * DOWN sums the same way over h, its K splits and the slots (up to 32 + top_k + 2 roundings);
+  * y rounds once: half a step of its type, relative to the value (and half the smallest
+    subnormal step).
 """
 import math
 
@@ -45,8 +45,10 @@ def _product(a, da, codes, s, z, bits):
     q, grp = codes.double(), torch.arange(K) // G
     sd, zd = s.double()[grp], z.double()[grp]
     w = (q - zd) * sd
-    mag = a.abs() @ ((128 + q + zd.abs()) * sd.abs())
-    err = ((G / 16 + 2) * 2 + 3 + groups + 8) * U * mag + da @ w.abs()
+    mag = a.abs() @ ((q + zd.abs()) * sd.abs())
+    top = torch.nn.functional.pad(a.abs() + da, (0, -K % 128)).view(len(a), -1, 128).amax(2)
+    da = da + 1.02 * 2.0 ** -15 * top.repeat_interleave(128, 1)[:, :K]
+    err = (13 + K / 32) * U * mag + da @ w.abs()
     return a @ w, err
 
 
@@ -69,13 +71,13 @@ def layer(p, bits, act, ids=None):
             else:
                 a = gate * 0.5 * torch.special.erfc(-gate / math.sqrt(2.0))
             h = a * up
-            dh = 1.13 * dg * up.abs() + a.abs() * du + 1.13 * dg * du + (16 * U + 2.0 ** -18) * h.abs() + 1e-37
+            dh = 1.13 * dg * up.abs() + a.abs() * du + 1.13 * dg * du + 16 * U * h.abs() + 1e-37
             part, dpart = _product(h, dh, *(v[e] for v in p["down"]), bits)
             c = float(p["weights"][t, j])
             y[t] += c * part[0]
             err[t] += abs(c) * dpart[0]
             mag[t] += abs(c) * part[0].abs()
-    err += (k + 2) * U * mag
+    err += (k + 34) * U * mag
     info = torch.finfo(dtype)
     return y, err + (y.abs() + err) * info.eps / 2 + info.smallest_normal * info.eps / 2
 

@@ -34,7 +34,7 @@ def test_route_argument_checks(libwq):
 def test_moe_argument_checks(libwq):
     L = libwq.lib()
     need = L.wq_moe_workspace_size(4, 2, 128, 256)
-    assert need >= 4 * 2 * (128 * 4 + 256 * 4)
+    assert need >= 4 * 2 * 128 * 2
     assert L.wq_moe_workspace_size(0, 2, 128, 256) == 0 and L.wq_moe_workspace_size(65, 2, 128, 256) == 0
     assert L.wq_moe_workspace_size(4, 17, 128, 256) == 0
 
@@ -44,6 +44,7 @@ def test_moe_argument_checks(libwq):
         return L.wq_moe(*a, T, K, I, N, E, k, bits, G, act, flags, ws,
                         ctypes.c_size_t(need if nbytes is None else nbytes), None)
     assert call(bits=3) == UNS and call(bits=5) == UNS and call(act=2) == UNS and call(G=16) == UNS
+    assert call(K=24576 + 64) == UNS and call(bits=8, G=16) == UNS
     for bad in (dict(T=0), dict(T=65, nbytes=1 << 40), dict(K=0), dict(K=252, G=-1), dict(I=0), dict(I=-8), dict(N=0),
                 dict(E=0), dict(E=513), dict(k=0), dict(k=17, nbytes=1 << 40), dict(G=0), dict(G=96), dict(flags=2),
                 dict(flags=8), dict(ws=None), dict(nbytes=need - 1), dict(I=1 << 30)):
@@ -53,7 +54,7 @@ def test_moe_argument_checks(libwq):
         assert call(**{name: P + 2}) == ALI
     assert call(N=252) == ALI and call(I=132, G=-1, bits=8) == ALI and call(ws=P + 16) == ALI
     if no_device():
-        assert call() == CUDA and call(G=-1, flags=4) == CUDA and call(bits=8, G=16, flags=5) == CUDA
+        assert call() == CUDA and call(G=-1, flags=4) == CUDA and call(bits=8, G=32, flags=5) == CUDA
 
 
 def test_logprobs_argument_checks(libwq):

@@ -13,7 +13,7 @@ CASES = [
     (1, 4, 2, 256, 128, 64, 4, 128, "fp16", "silu", False),
     (1, 8, 8, 512, 384, 520, 4, 128, "bf16", "gelu", False),
     (2, 5, 3, 288, 96, 72, 4, 32, "fp16", "gelu", True),
-    (3, 6, 2, 80, 48, 136, 8, 16, "fp16", "silu", True),
+    (3, 6, 2, 96, 64, 136, 8, 32, "fp16", "silu", True),
     (4, 4, 4, 256, 256, 64, 8, 128, "bf16", "silu", True),       # 4 slots on every expert
     (5, 12, 3, 1112, 744, 1000, 4, -1, "bf16", "gelu", False),   # K ends inside a tile
     (5, 7, 2, 20, 24, 40, 8, -1, "fp16", "silu", False),         # K = 5 word rows
@@ -22,9 +22,13 @@ CASES = [
     (16, 2, 2, 256, 192, 104, 4, 64, "fp16", "silu", True),      # 16: full blocks
     (17, 1, 1, 128, 64, 64, 4, 64, "bf16", "gelu", False),       # 17 tokens on one expert: two blocks
     (33, 40, 1, 64, 64, 64, 8, 64, "fp16", "silu", False),       # more than 32 slots
-    (48, 32, 4, 256, 176, 128, 8, 16, "bf16", "silu", True),
+    (48, 32, 4, 256, 192, 128, 8, 32, "bf16", "silu", True),
     (64, 16, 16, 64, 32, 64, 4, 32, "fp16", "silu", False),      # 1024 slots, 64 tokens on every expert
     (64, 512, 2, 32, 32, 8, 4, 32, "bf16", "silu", False),       # as many experts as there can be
+    (7, 3, 2, 8256, 32, 16, 4, 32, "bf16", "silu", False),       # a long K: two slots per block
+    (2, 2, 1, 20000, 16, 8, 8, -1, "fp16", "silu", False),       # one slot per block
+    (6, 2, 1, 64, 6176, 24, 4, 32, "fp16", "silu", True),        # a long inner length: K splits
+    (1, 2, 2, 32, 8776, 16, 8, -1, "bf16", "gelu", False),
 ]
 
 
@@ -86,13 +90,13 @@ def test_empty_slots(cuda, libwq, T):
 @pytest.mark.parametrize("T", [4, 12, 24])
 def test_the_same_expert_twice(cuda, libwq, T):
     import torch
-    p = moe_oracle.problem(T, 4, 3, 64, 32, 64, 8, 16, torch.float16, seed=9)
+    p = moe_oracle.problem(T, 4, 3, 64, 32, 64, 8, 32, torch.float16, seed=9)
     ids = p["ids"].clone()
     ids[:, 2] = ids[:, 0]
     ids[1] = 3
     ref, tol = moe_oracle.layer(p, 8, "silu", ids)
     (x, _, weights), w = moe_oracle.to_gpu(libwq, p, 8, cuda)
-    moe_oracle.assert_close(libwq.moe(x, ids.to(cuda), weights, *w, 8, 16), ref, tol)
+    moe_oracle.assert_close(libwq.moe(x, ids.to(cuda), weights, *w, 8, 32), ref, tol)
 
 
 def test_extreme_zero_points_and_scales(cuda, libwq):
@@ -108,6 +112,41 @@ def test_extreme_zero_points_and_scales(cuda, libwq):
     ref, tol = moe_oracle.layer(p, 4, "gelu")
     (x, ids, weights), w = moe_oracle.to_gpu(libwq, p, 4, cuda)
     moe_oracle.assert_close(libwq.moe(x, ids, weights, *w, 4, 32, activation="gelu"), ref, tol)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_values_of_very_different_size(cuda, libwq, dt):
+    """Blocks with one large value, tiny blocks, zeros, and the type's own limits."""
+    import torch
+    p = moe_oracle.problem(5, 3, 2, 512, 64, 48, 4, 32, _dtype(dt), seed=14)
+    info = torch.finfo(p["x"].dtype)
+    p["x"][0, 7] = 2000.0
+    p["x"][1, 128:256] *= 2.0 ** -12
+    p["x"][2] = 0
+    p["x"][3, ::3] = 0
+    p["x"][4] = (p["x"][4].float() * (info.max / 1e6 if dt == "fp16" else 1e-30)).to(p["x"].dtype)
+    ref, tol = moe_oracle.layer(p, 4, "silu")
+    (x, ids, weights), w = moe_oracle.to_gpu(libwq, p, 4, cuda)
+    y = libwq.moe(x, ids, weights, *w, 4, 32)
+    moe_oracle.assert_close(y, ref, tol)
+    assert (y[2] == 0).all()
+
+
+def test_the_largest_values(cuda, libwq):
+    """bf16 values next to the type's maximum: the fixed-point step has the next exponent.  With
+    s = 2^-75 gate and up stay below 32 * 16 * 2^128 * 2^-75 = 2^62, so h below 2^124 is in fp32's
+    range (with 2^-70 it is not: the 64-bit h of these inputs reaches 1.36e39)."""
+    import torch
+    p = moe_oracle.problem(2, 1, 1, 32, 32, 8, 4, 32, torch.bfloat16, seed=15)
+    p["x"][:] = torch.finfo(torch.bfloat16).max
+    p["x"][1] *= -1
+    for name in ("up", "down"):
+        p[name][1].fill_(2.0 ** -75)
+    ref, tol = moe_oracle.layer(p, 4, "gelu")
+    (x, ids, weights), w = moe_oracle.to_gpu(libwq, p, 4, cuda)
+    y = libwq.moe(x, ids, weights, *w, 4, 32, activation="gelu")
+    assert torch.isfinite(y).all()
+    moe_oracle.assert_close(y, ref, tol)
 
 
 def test_hidden_values_beyond_fp16(cuda, libwq):
@@ -133,7 +172,7 @@ def test_a_row_that_is_not_finite_stays_alone(cuda, libwq, T):
     x[3, 0] = float("inf")
     y = libwq.moe(x, ids, weights, *w, 4, 32)
     keep = [t for t in range(T) if t not in (1, 3)]
-    assert torch.isnan(y[1]).all() and not torch.isfinite(y[3]).any()
+    assert torch.isnan(y[1]).all() and torch.isnan(y[3]).all()
     moe_oracle.assert_close(y[keep], ref[keep], tol[keep])
 
 
@@ -192,7 +231,7 @@ def test_refusals(cuda, libwq):
             plan(*a)
     with pytest.raises(ValueError):
         plan(x, ids, weights, out=torch.empty((2, 40), dtype=x.dtype, device=cuda))
-    for bits, G in ((3, 32), (4, 24), (4, 0), (8, 32)):
+    for bits, G in ((3, 32), (4, 24), (4, 0), (8, 32), (4, 64)):
         with pytest.raises((ValueError, libwq.WQError)):
             libwq.moe(x, ids, weights, *w, bits, G)
     with pytest.raises(ValueError):
