@@ -614,32 +614,41 @@ def gptqmodel_quantized_matmul(x, qweight, qzeros, scales, bits: int, group_size
 
 # --------------------------------------------------- mixture of experts, log probabilities
 
-def _on_current(t, name: str):
-    """The library launches on the current device: a tensor of another one is refused."""
-    if t.get_device() != _torch().cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_torch().cuda.current_device()}")
+def _on_current(t, name: str) -> int:
+    """The tensor's device, which has to be the current one: the library launches there."""
+    torch = _torch()
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+_LOGIT_TYPES = {}
 
 
 def _logits(logits):
-    """Type, rows, columns and row stride of a 2-d tensor of logits, whose rows are contiguous."""
+    """Type, rows, columns, row stride and device of a 2-d tensor of logits, whose rows are contiguous."""
     torch = _torch()
+    if not _LOGIT_TYPES:
+        _LOGIT_TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits must be a torch.Tensor")
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor (there is no CPU path)")
-    kind = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(logits.dtype)
+    kind = _LOGIT_TYPES.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
     if logits.dim() != 2:
         raise ValueError("logits must be a 2-d tensor")
     rows, cols = logits.shape
-    if cols > 1 and logits.stride(1) != 1:
+    ld, inner = logits.stride()
+    if cols > 1 and inner != 1:
         raise ValueError("the rows of logits must be contiguous")
-    ld = logits.stride(0) if rows > 1 else cols
+    if rows <= 1:
+        ld = cols
     if ld < cols:
         raise ValueError("the rows of logits overlap")
-    _on_current(logits, "logits")
-    return kind, rows, cols, ld
+    return kind, rows, cols, ld, _on_current(logits, "logits")
 
 
 def moe_route(logits, top_k: int, renormalize: bool = True, scale: float = 1.0, pdl: bool = False):
@@ -652,12 +661,15 @@ def moe_route(logits, top_k: int, renormalize: bool = True, scale: float = 1.0, 
     them.  A logit of -inf or NaN is never chosen: where fewer than ``top_k``
     experts are left the slot is empty, id -1 and weight 0."""
     torch = _torch()
-    kind, T, E, ld = _logits(logits)
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    st = lib().wq_moe_route(logits.data_ptr(), kind, T, E, ld, top_k, 1 if renormalize else 0, float(scale),
-                            ids.data_ptr(), weights.data_ptr(), WQ_FLAG_PDL if pdl else 0, _stream())
-    _check("wq_moe_route", st)
+    kind, T, E, ld, dev = _logits(logits)
+    where = logits.device
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=where)
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=where)
+    st = lib().wq_moe_route(logits.data_ptr(), kind, T, E, ld, top_k, 1 if renormalize else 0, scale,
+                            ids.data_ptr(), weights.data_ptr(), WQ_FLAG_PDL if pdl else 0,
+                            torch._C._cuda_getCurrentRawStream(dev))
+    if st != 0:
+        raise WQError("wq_moe_route", st)
     return ids, weights
 
 
@@ -721,32 +733,51 @@ class MoePlan:
         self._dev = w_up.get_device()
         self._run = lib().wq_moe
         self._bytes = [0] + [int(lib().wq_moe_workspace_size(T, top_k, I, N)) for T in range(1, tokens + 1)]
+        self._types = (torch.int32, torch.float32, torch.uint8)
 
-    def __call__(self, x, ids, weights, out=None):
-        torch = _torch()
+    def _refuse(self, x, ids, weights):
+        """Say what is wrong with a call's tensors."""
+        int32, float32, _ = self._types
         _need(x, self.dtype, "x")
-        _need(ids, torch.int32, "ids")
-        _need(weights, torch.float32, "weights")
-        T, d = x.shape[0], self._dev
+        _need(ids, int32, "ids")
+        _need(weights, float32, "weights")
+        T = x.shape[0]
         if x.shape[1] != self.K or not 1 <= T <= self.tokens:
             raise ValueError(f"x has shape {tuple(x.shape)}; needs (1 to {self.tokens}, {self.K})")
         if ids.shape != (T, self.top_k) or weights.shape != (T, self.top_k):
             raise ValueError(f"ids and weights have shapes {tuple(ids.shape)} and {tuple(weights.shape)}; "
                              f"need {(T, self.top_k)}")
+        _on_current(x, "x")
+        raise ValueError(f"all tensors must be on the weights' device {self.device}")
+
+    def __call__(self, x, ids, weights, out=None):
+        torch = _torch()
+        dev, k, dt = self._dev, self.top_k, self.dtype
+        int32, float32, uint8 = self._types
+        try:   # every rule in one expression; _refuse names the broken one
+            T = x.shape[0]
+            good = (x.dtype is dt and x.shape == (T, self.K) and 1 <= T <= self.tokens and x.is_contiguous()
+                    and ids.dtype is int32 and ids.shape == (T, k) and ids.is_contiguous()
+                    and weights.dtype is float32 and weights.shape == (T, k) and weights.is_contiguous()
+                    and x.get_device() == dev and ids.get_device() == dev and weights.get_device() == dev
+                    and torch._C._cuda_getDevice() == dev)
+        except (AttributeError, IndexError):
+            good = False
+        if not good:
+            self._refuse(x, ids, weights)
         if out is None:
-            out = torch.empty((T, self.N), dtype=self.dtype, device=self.device)
+            out = torch.empty(T, self.N, dtype=dt, device=self.device)
         else:
-            _need(out, self.dtype, "out")
+            _need(out, dt, "out")
             if out.shape != (T, self.N):
                 raise ValueError(f"out has shape {tuple(out.shape)}; needs {(T, self.N)}")
-        if x.get_device() != d or ids.get_device() != d or weights.get_device() != d or out.get_device() != d:
-            raise ValueError(f"all tensors must be on the weights' device {self.device}")
-        _on_current(x, "x")
+            _same_device(x, out=out)
         nbytes = self._bytes[T]
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        ws = torch.empty(nbytes, dtype=uint8, device=self.device)
         K, I, N, E, top_k, bits, group_size, act, flags = self._shape
         st = self._run(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), *self._weights, out.data_ptr(), T, K, I, N,
-                       E, top_k, bits, group_size, act, flags, ws.data_ptr(), nbytes, _stream())
+                       E, top_k, bits, group_size, act, flags, ws.data_ptr(), nbytes,
+                       torch._C._cuda_getCurrentRawStream(dev))
         if st != 0:
             raise WQError("wq_moe", st)
         return out
@@ -775,24 +806,29 @@ def logprobs(logits, tokens=None, top_k: int = 0, pdl: bool = False):
     ``top_id`` (R, top_k) int64, in the order (logit descending, index
     ascending).  A row of nothing but -inf, or with NaN or +inf, is NaN."""
     torch = _torch()
-    kind, R, V, ld = _logits(logits)
+    kind, R, V, ld, dev = _logits(logits)
     if not 0 <= top_k <= min(V, 32):
         raise ValueError(f"top_k must be 0 to {min(V, 32)}, got {top_k}")
-    dev = logits.device
-    out = {"entropy": torch.empty(R, dtype=torch.float32, device=dev)}
+    where, f32 = logits.device, torch.float32
+    entropy = torch.empty(R, dtype=f32, device=where)
+    out = {"entropy": entropy}
+    tok = lp = top_lp = top_id = None
     if tokens is not None:
         _need(tokens, torch.int64, "tokens", ndim=1)
-        _same_device(logits, tokens=tokens)
         if tokens.shape[0] != R:
             raise ValueError(f"tokens has shape {tuple(tokens.shape)}; needs ({R},)")
-        out["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
+        if tokens.get_device() != dev:
+            raise ValueError(f"tokens is on {tokens.device}, logits on {where}: all tensors must share one device")
+        out["logprob"] = t = torch.empty(R, dtype=f32, device=where)
+        tok, lp = tokens.data_ptr(), t.data_ptr()
     if top_k:
-        out["top_logprob"] = torch.empty((R, top_k), dtype=torch.float32, device=dev)
-        out["top_id"] = torch.empty((R, top_k), dtype=torch.int64, device=dev)
-    st = lib().wq_logprobs(logits.data_ptr(), kind, R, V, ld, _ptr(tokens), top_k, _ptr(out.get("logprob")),
-                           out["entropy"].data_ptr(), _ptr(out.get("top_logprob")), _ptr(out.get("top_id")),
-                           WQ_FLAG_PDL if pdl else 0, _stream())
-    _check("wq_logprobs", st)
+        out["top_logprob"] = t = torch.empty(R, top_k, dtype=f32, device=where)
+        out["top_id"] = u = torch.empty(R, top_k, dtype=torch.int64, device=where)
+        top_lp, top_id = t.data_ptr(), u.data_ptr()
+    st = lib().wq_logprobs(logits.data_ptr(), kind, R, V, ld, tok, top_k, lp, entropy.data_ptr(), top_lp, top_id,
+                           WQ_FLAG_PDL if pdl else 0, torch._C._cuda_getCurrentRawStream(dev))
+    if st != 0:
+        raise WQError("wq_logprobs", st)
     return out
 
 

@@ -69,8 +69,8 @@ namespace {
 
 constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
 constexpr int MAXBT = 8;        // slots per block
-#ifndef FEW_TILES
-#define FEW_TILES 300
+#ifndef SOLO_T
+#define SOLO_T 16
 #endif
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
@@ -363,7 +363,10 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     constexpr int RPS = step_rows<BITS>();       // 4 or 8
     constexpr int RL = RPS / 4;                  // word rows per lane and step
     constexpr int SPS = BOX_ROWS / RPS;          // steps per stage
-    constexpr int WC = MW / WK;                  // warps along the columns
+    // DOWN with WK = 1: every warp works alone, on the tile's 64 columns and its own share of the (block, K) line,
+    // and sums y in its own copy: no barrier until the end.
+    constexpr bool SOLO = !UP && WK == 1;
+    constexpr int WC = SOLO ? 1 : MW / WK;       // warps along the columns
     constexpr int TC = MCOLS * WC;               // weight columns per tile
     extern __shared__ uint8_t smem_raw[];
     // the 128-byte swizzle of the TMA boxes repeats every 1024 bytes
@@ -376,7 +379,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     // 16-byte column chunk of this lane (columns 4 cg .. 4 cg + 3 of each half): with the lines of a
     // stage below, the eight lanes of a quarter-warp meet eight different bank groups
     const int cg = UP ? g : ((g & 1) << 2) | (g >> 1);
-    const int wk = warp / WC, wc = warp % WC;
+    const int wk = SOLO ? 0 : warp / WC, wc = warp % WC;
     uint64_t* const bar = bars + warp * NST;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) mbar_init(&bar[i], 1);
@@ -391,17 +394,25 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const int rank = UP ? 0 : (int)blockIdx.x % p.cluster;
     const uint32_t sz_bytes = 256u * (uint32_t)p.sz_rows;   // a stage's s rows, then its z rows
     const uint32_t roff = MW * NST * (STAGE + sz_bytes);    // behind the rings
-    uint8_t* const tab = smem + roff + table_at(MW, p.bt);
+    constexpr int RW = SOLO ? 0 : MW;   // warps with partials in shared memory
+    uint8_t* const tab = smem + roff + table_at(RW, p.bt);
     const int ts = table_slots(p.S);
     int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
     const Blocks blk{&head, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
     if constexpr (UP) find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), p.ntiles, blockIdx.x, gridDim.x);
     else find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), Q4, rank, p.cluster);
+    int at0 = head.i0, end = head.i1;
+    if constexpr (SOLO) {
+        at0 = end = 0;
+        if (head.n > 0) {
+            at0 = share(blk, Q4, rank * MW + warp, p.cluster * MW);
+            end = share(blk, Q4, rank * MW + warp + 1, p.cluster * MW);
+        }
+    }
     // ---- this CTA's items.  UP: (block, tile) pairs, all steps of K; DOWN: one tile, runs of a block's steps.
     struct Item {
         int at, u, tile, s0, ns;   // position on the line, block, column tile, first step, steps
     };
-    const int end = head.i1;
     auto open = [&](Item& it) {    // the item at it.at
         if constexpr (UP) {
             it.u = it.at / p.ntiles;
@@ -419,6 +430,10 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     auto next = [&](Item& it) { it.at += UP ? 1 : (it.ns + XBLK - 1) / XBLK; };
     // steps of this warp in an item: [first, first + count), whole fixed-point blocks
     auto range = [&](const Item& it, int& first) {
+        if constexpr (SOLO) {
+            first = it.s0;
+            return it.ns;
+        }
         const int per = ((it.ns + WK - 1) / WK + XBLK - 1) / XBLK * XBLK;
         first = min(it.ns, wk * per);
         const int n = min(it.ns, first + per) - first;
@@ -431,7 +446,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (NST * STAGE);
     const uint32_t sz_ring = smem_u32(smem) + MW * NST * STAGE + (uint32_t)warp * (NST * sz_bytes);
     Item wit;
-    wit.at = head.i0;
+    wit.at = at0;
     int wq = 0, wleft = 0, wslot = 0;   // next step, stages left in the item, ring slot
     bool ok = true, wopen = false;
     auto issue = [&]() {
@@ -467,9 +482,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
 
     if constexpr (!UP) grid_dependency_wait();   // h
     float* const red = reinterpret_cast<float*>(smem + roff);   // [wk][slot][TC]
-    const uint32_t xoff = roff + values_at(MW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
+    const uint32_t xoff = roff + values_at(RW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
     float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));         // UP: [slot][block]
-    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [T][TC]
+    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [T][TC], SOLO: one per warp
     // This lane's 16-byte vectors of word row t (and t + 4): line r of 128 bytes holds them at chunk
     // cg ^ (r & 7).  UP: the lines of a word row's two halves follow each other; DOWN: 16 lines each.
     constexpr uint32_t HALF = UP ? 128u : STAGE / 2, LINE = UP ? 256u : 128u;   // to the other half, to the next row
@@ -482,11 +497,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     int rslot = 0, phase = 0;   // ring position of the next stage to read
 
     if constexpr (!UP)
-        for (int i = threadIdx.x; i < p.T * TC; i += MT) ys[i] = 0.0f;   // (a barrier precedes their first use)
+        for (int i = threadIdx.x; i < p.T * TC * (SOLO ? MW : 1); i += MT) ys[i] = 0.0f;
+    if constexpr (SOLO) __syncthreads();   // (elsewhere a barrier precedes their first use)
 
     int block = -1;   // UP: the block whose values are in shared memory
     Item it;
-    for (it.at = head.i0; it.at < end; next(it)) {
+    for (it.at = at0; it.at < end; next(it)) {
         open(it);
         int q0;
         const int nq = range(it, q0);
@@ -743,6 +759,33 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 rslot ^= 1;
                 phase ^= rslot == 0;
             }
+            if constexpr (SOLO) {
+                // y += weight * row, in the warp's own sums; slots that share a token lie in different lanes t or n,
+                // which take turns
+                float* const mine = ys + warp * p.T * TC;
+#pragma unroll
+                for (int n = 0; n < AT; ++n)
+#pragma unroll 1
+                    for (int turn = 0; turn < 4; ++turn) {
+                        const int pos = 4 * n + turn;
+                        if (pos < bm && t == turn) {
+                            const int sl = slots[pos];
+                            const float a = p.weights[sl];
+                            float* const row = mine + sl / p.top_k * TC + 4 * cg;
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                float4 v = *reinterpret_cast<float4*>(row + 32 * hf);
+                                v.x = fmaf(a, acc[hf][0][n], v.x);
+                                v.y = fmaf(a, acc[hf][1][n], v.y);
+                                v.z = fmaf(a, acc[hf][2][n], v.z);
+                                v.w = fmaf(a, acc[hf][3][n], v.w);
+                                *reinterpret_cast<float4*>(row + 32 * hf) = v;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                return;
+            }
             // ---- the warps' partials meet in shared memory
 #pragma unroll
             for (int n = 0; n < AT; ++n) {
@@ -756,6 +799,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         };
         if (NT == 1 || bm <= 4) run(std::integral_constant<int, 1>{});
         else run(std::integral_constant<int, NT>{});
+        if constexpr (SOLO) continue;
         __syncthreads();
         if constexpr (UP) {
             // The tile's TC / 2 values of h of one slot are one fixed-point block (128 or 64): LPS lanes, 4 each
@@ -831,6 +875,21 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         }
     if constexpr (!UP) {
         // ---- the tile's CTAs join their sums, in their order; each writes its share of the rows
+        if constexpr (SOLO) {   // first the warps', in theirs
+            __syncthreads();
+            for (int i = threadIdx.x; i < p.T * (TC / 4); i += MT) {
+                float4 v = *reinterpret_cast<const float4*>(ys + 4 * i);
+#pragma unroll
+                for (int w = 1; w < MW; ++w) {
+                    const float4 o = *reinterpret_cast<const float4*>(ys + w * p.T * TC + 4 * i);
+                    v.x += o.x;
+                    v.y += o.y;
+                    v.z += o.z;
+                    v.w += o.w;
+                }
+                *reinterpret_cast<float4*>(ys + 4 * i) = v;
+            }
+        }
         if (p.cluster > 1) cluster_sync();
         else __syncthreads();
         const int tl = (int)blockIdx.x / p.cluster;
@@ -883,19 +942,25 @@ void cut_smem(Cut& c, bool up, int T, int S, int Q) {
     c.xcol = up ? xcol_bytes(Q) : 0;
     c.nsteps = up ? (Q + XBLK - 1) / XBLK : 0;
     c.smem = ring_bytes(c.W, c.sz_rows) + (up ? steps_at(c.W, c.bt, S, c.xcol) + c.bt * c.nsteps * 4
-                                              : values_at(c.W, c.bt, S) + T * MCOLS * (c.W / c.WK) * 4);
+                                              : values_at(c.WK == 1 ? 0 : c.W, c.bt, S) + T * MCOLS * (c.W / c.WK) * 4);
 }
 
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
-// leave room for (bt = 0: K is too long).  Few tokens and tiles: CTAs of 8 warps, beside which DOWN's find room
-// while they run; else of 16, 4 of them along K or 8, what leaves fewer steps idle.
+// leave room for (bt = 0: K is too long).
+//  * Few tokens, and no more tiles of 64 values of h than SMs: CTAs of 8 warps, beside which DOWN's start while
+//    they run (1 token, 8 experts of 2048 x 1024: 16.2 us against 19.7 us with 16 warps; with 344 tiles, 2 experts of
+//    4096 x 11008, 59 us against 45 us).
+//  * Else 16 warps: 4 along K, with tiles of 128 values, unless 8 leave fewer steps idle.  (8 with tiles of 64 also
+//    where that fills the SMs' last round better measured slower: DOWN's shorter fixed-point blocks cost more. 16
+//    tokens, 64 experts of 2048 x 1024: 96 us against 81 us.)
 Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
-    const int Q = (K + SK - 1) / SK;
+    const int Q = (K + SK - 1) / SK, sms = sm_count();
+    const long long slots = std::min(S, E), tiles = (I + 63) / 64;   // of 64 values
     Cut c{};
     c.spg = group_size == -1 || group_size == K ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
     c.cluster = 1;
-    if (T <= 4 && (long long)((I + 63) / 64) * std::min(S, E) <= FEW_TILES) {
+    if (T <= 4 && tiles * slots <= sms) {
         c.W = 8;
         c.WK = 4;
         c.bt = 4;
@@ -954,7 +1019,9 @@ Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
     c.spg = group_size == -1 || group_size == I ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
     int best = -1;   // places taken, in percent
+    const bool solo = T <= SOLO_T;
     for (const int WK : {8, 4}) {
+        if (solo && WK == 4) continue;
         const int tiles = (N + MCOLS * c.W / WK - 1) / (MCOLS * c.W / WK);
         for (int cs = 1; cs <= 8; ++cs) {
             const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
@@ -966,6 +1033,13 @@ Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
                 c.cluster = cs;
             }
         }
+    }
+    if (solo) {
+        c.WK = 1;
+        c.bt = T <= 4 ? 4 : MAXBT;
+        cut_smem(c, false, T, S, 0);
+        if (c.smem <= max_smem(8)) return c;
+        c.WK = 8;
     }
     // (many tokens and small groups: narrow tiles, then blocks of fewer slots; 2 always fit)
     for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; c.bt /= 2) {
@@ -1042,7 +1116,8 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
     const int warp_tiles = UP ? (p.I + 31) / 32 : (p.NW + MCOLS - 1) / MCOLS;   // of 64 columns
     auto go = [&](auto nt, auto w, auto wk) {
         constexpr int NT = decltype(nt)::value, W = decltype(w)::value, WK = decltype(wk)::value;
-        p.ntiles = (warp_tiles + W / WK - 1) / (W / WK);
+        constexpr int across = WK == 1 ? 1 : W / WK;   // warps along the columns
+        p.ntiles = (warp_tiles + across - 1) / across;
         return launch_one<BITS, BF, NT, UP, W, WK>(tm, p, c.smem, pdl, stream);
     };
     using N1 = std::integral_constant<int, 1>;
@@ -1055,7 +1130,11 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
         if (c.bt <= 4) return c.WK == 4 ? go(N1{}, N16{}, N4{}) : go(N1{}, N16{}, N8{});
         return c.WK == 4 ? go(N2{}, N16{}, N4{}) : go(N2{}, N16{}, N8{});
     } else {
-        if (c.bt <= 4) return c.WK == 4 ? go(N1{}, N8{}, N4{}) : go(N1{}, N8{}, N8{});
+        if (c.bt <= 4) {
+            if (c.WK == 1) return go(N1{}, N8{}, N1{});
+            return c.WK == 4 ? go(N1{}, N8{}, N4{}) : go(N1{}, N8{}, N8{});
+        }
+        if (c.WK == 1) return go(N2{}, N8{}, N1{});
         return c.WK == 4 ? go(N2{}, N8{}, N4{}) : go(N2{}, N8{}, N8{});
     }
 }
@@ -1065,10 +1144,22 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
     MoeParams p{};
     p.x = m.x; p.ids = m.ids; p.weights = m.weights; p.y = m.y;
     p.T = m.T; p.top_k = m.top_k; p.S = m.T * m.top_k; p.E = m.E; p.I = m.I; p.act = m.act;
-    const Cut up = cut_up(m.T, p.S, p.E, m.K, m.I, m.group_size, BITS);
+    // the cuts of this thread's last shape: a decode loop asks for the same ones again
+    struct Plan {
+        int T, S, E, K, I, N, group_size, sms;
+        Cut up, down;
+    };
+    static thread_local Plan last{};
+    const int sms = sm_count();
+    if (last.T != p.T || last.S != p.S || last.E != p.E || last.K != m.K || last.I != m.I || last.N != m.N ||
+        last.group_size != m.group_size || last.sms != sms) {
+        last = Plan{p.T, p.S, p.E, m.K, m.I, m.N, m.group_size, sms, {}, {}};
+        last.up = cut_up(m.T, p.S, p.E, m.K, m.I, m.group_size, BITS);
+        last.down = cut_down(m.T, p.S, m.I, m.N, m.group_size, BITS, last.up.W == 8);
+    }
+    const Cut up = last.up, down = last.down;
     p.Qh = (m.I + SK - 1) / SK;
     p.hb = MCOLS * (up.W / up.WK) / 2 / SK;   // a tile of UP: 128 values or 64
-    const Cut down = cut_down(m.T, p.S, m.I, m.N, m.group_size, BITS, up.W == 8);
     if (up.bt == 0 || down.bt == 0) return WQ_ERR_UNSUPPORTED;
     p.hq = static_cast<int8_t*>(m.ws);
     p.hstep = reinterpret_cast<float*>(p.hq + (size_t)2 * p.S * p.Qh * SK);
