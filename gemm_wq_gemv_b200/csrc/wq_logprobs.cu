@@ -35,12 +35,7 @@ __device__ unsigned int g_logprobs_status = 0;
 
 namespace {
 
-#ifndef LPT
-#define LPT 256
-#define LPB 5
-#define LPU 4
-#endif
-constexpr int LT = LPT;        // threads per CTA
+constexpr int LT = 256;        // threads per CTA
 constexpr int LW = LT / 32;
 constexpr int CAP = 1024;      // entries at or above the floor that are ranked at once
 constexpr int MAXK = 32;
@@ -151,11 +146,11 @@ __device__ __forceinline__ unsigned long long pack_key(uint32_t key, uint32_t in
 }
 
 template <int TYPE, int CS>
-__global__ void __launch_bounds__(LT, LPB) logprobs_kernel(const LpParams p) {
+__global__ void __launch_bounds__(LT, 5) logprobs_kernel(const LpParams p) {
     using L = Logit<TYPE>;
     using VT = Vec<TYPE>;
     constexpr int VN = VT::N;
-    constexpr int U = LPU;  // vectors in flight per thread
+    constexpr int U = 4;  // vectors in flight per thread
     __shared__ LpShared sh;
     grid_dependency_wait();
     grid_launch_dependents();

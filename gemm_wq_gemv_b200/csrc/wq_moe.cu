@@ -7,21 +7,23 @@
 // with W = (q - z) * s as everywhere in this library.  A slot whose id lies
 // outside 0 .. E-1 is empty and adds nothing.
 //
-// Two launches of one kernel template.  UP turns x into h (one row per slot),
-// DOWN turns h into y.  Both are meant to be bound by HBM: the layer reads
-// each chosen expert's words once.
+// Two launches of one kernel template.  UP turns x into h (one row per slot), DOWN
+// turns h into y.  The layer reads each chosen expert's words once and is meant to
+// be bound by HBM.
 //  * Work split.  Slots are grouped by expert into blocks of bt slots (up to 8;
-//    fewer when K is very long), so an expert's words are read once for them.
-//    Every CTA (16 warps, one per SM) derives the blocks from the ids.  UP: the
-//    (block, column tile) pairs, all of K each, are dealt out over the SMs in equal
-//    runs.  DOWN: a column tile belongs to a cluster of up to 8 CTAs, among which the
-//    tile's (block, part of K) line is dealt out; they sum y, weighted, in shared
-//    memory and join the sums through distributed shared memory, in a fixed order.
-//    (Rows per slot in global memory, summed by the last CTA to arrive, cost 1 us
-//    per item for the fence and up to 17 us at the end.)  A CTA's warps are WK along
-//    K times 16 / WK along the columns, 64 columns each (UP: 32 gate and the matching
-//    32 up columns, so the activation needs no second pass); their partials meet in
-//    shared memory while the loads of the next item run.
+//    fewer when K is very long), so an expert's words are read once for them.  Every
+//    CTA derives the blocks from the ids.  UP (one CTA of 16 warps per SM): the
+//    (block, column tile) pairs, all of K each, are dealt out over the SMs in runs of
+//    equal weight.  DOWN (two CTAs of 8 warps per SM): a tile of 64 columns belongs to
+//    a cluster of up to 8 CTAs, among whose warps the tile's (block, part of K) line is
+//    dealt out; every warp sums y, weighted, in its own copy in shared memory, and the
+//    copies are joined at the end, across the cluster through distributed shared
+//    memory, in a fixed order.  (Rows per slot in global memory, summed by the last
+//    CTA to arrive, cost 1 us per item for the fence and up to 17 us at the end.)
+//    Where no copies fit (more than 16 tokens), and in UP, the warps split K or the
+//    tile's columns, 64 columns each (UP: 32 gate and the matching 32 up columns, so
+//    the activation needs no second pass), and their partials meet in shared memory
+//    while the loads of the next item run.
 //  * Products on integers.  Unpacking codes to fp16 or bf16 costs 7 instructions
 //    per word of 8 codes, and with m16n8k16 (2.1 clocks per SM on B200) that held
 //    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
@@ -36,17 +38,23 @@
 //    block, so a product moves by about 3e-5 of itself, a tenth of the rounding of
 //    an fp16 output.  UP converts x once per block of slots, while its first words
 //    arrive, and leaves h converted (a tile's 128 values of a slot, or 64, are one
-//    block), so that DOWN copies bytes.  A block with a value that is not finite gets the step NaN.
+//    block), so that DOWN only reads bytes.  A block with a value that is not finite
+//    gets the step NaN.
 //  * One more MMA per step with A = 1 gives X, the tokens' sums, so that a zero
 //    point of any value costs nothing per code.  At the end of a block (or group):
 //    acc += s * step * (D - z X) in fp32, D = 256 D_hi + D_lo.
 //  * Loads.  A warp's words come by TMA, 16 word rows x 64 columns per stage (4 KB)
 //    with the s and z rows of its groups, into a private ring of two stages: 64 to
-//    128 KB in flight per SM.  The 128-byte swizzle and the column order of the
-//    lanes (chunk cg) keep the 16-byte reads free of bank conflicts.  (cp.async by every lane, which
-//    this replaced, cost 19 instructions per step of 32 values, a quarter of all.)
+//    128 KB in flight per SM.  The 128-byte swizzle and the column order of the lanes
+//    (chunk cg) keep the 16-byte reads free of bank conflicts.  (cp.async by every
+//    lane, which this replaced, cost 19 instructions per step of 32 values, a quarter
+//    of all.)
 //  * DOWN is a programmatic dependent of UP: it finds its blocks and requests its
 //    first words while UP drains, and waits only before it reads h.
+// Measured (B200): 16 tokens, 2 of 8 experts of 4096 x 11008, 4-bit, 569 MB: 152 us,
+// 3.7 TB/s; UP reads at 4.8 TB/s and is held by its last round of items and, where an
+// expert has more than 4 tokens, by instruction issue (a second MMA per operand and
+// twice the folds); DOWN by instruction issue.
 // Every mbarrier wait is bounded; on time-out the kernel records it in its status
 // word and skips the rest of the warp's work.
 #include <cuda_bf16.h>
@@ -69,9 +77,7 @@ namespace {
 
 constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
 constexpr int MAXBT = 8;        // slots per block
-#ifndef SOLO_T
-#define SOLO_T 16
-#endif
+constexpr int SOLO_T = 16;      // most tokens for which every warp of DOWN keeps sums of its own
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
 constexpr int BOX_ROWS = 16;    // word rows per TMA box
@@ -141,6 +147,33 @@ __device__ __forceinline__ void mma_u8s8(bool first, int (&d)[4], uint32_t a0, u
         asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// Two floats at once (one instruction each: the folds below are bound by instruction issue).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // The blocks of a launch: experts in the order of their first slot (S <= 32) or of their
@@ -580,13 +613,11 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         // ---- one item.  AT: token tiles that hold slots of this block
         auto run = [&](auto at_tag) {
             constexpr int AT = decltype(at_tag)::value;
-            float acc[2][4][AT];
+            uint64_t acc[2][2][AT];   // two columns each
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int n = 0; n < AT; ++n) acc[hf][c][n] = 0.0f;
+                for (int n = 0; n < AT; ++n) acc[hf][0][n] = acc[hf][1][n] = 0ull;
             // B column g of token tile n: UP from shared memory; DOWN straight from global memory, a stage ahead (every
             // CTA reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
             uint32_t xa[AT], sp[AT];               // UP
@@ -623,7 +654,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             // as a float, that much more (128 * 255 * 128 < 2^22), so no conversion is needed.
             constexpr int BIAS = 0x4B400000;
             auto sum_value = [](int hi, int lo) {
-                return fmaf(256.0f, __int_as_float(hi) - 12582912.0f, __int_as_float(lo) - 12582912.0f);
+                const float2 v = unpack2(add2(pack2(__int_as_float(hi), __int_as_float(lo)), pack2(-12582912.0f, -12582912.0f)));
+                return fmaf(256.0f, v.x, v.y);
             };
             auto clear = [&]() {
 #pragma unroll
@@ -681,28 +713,29 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             };
             // the block (or the group) ends: acc += s step (D - z X)
             auto fold = [&](int i, int k, uint32_t sz) {   // k: the block's place in the stage; sz: the group's s row in it
-                float step[AT], X[AT];
+                uint64_t step[AT], X[AT];   // twice each; X negated
 #pragma unroll
                 for (int n = 0; n < AT; ++n) {
-                    step[n] = UP ? __uint_as_float(lds32_u32(sp[n] + 4u * (i / XBLK))) : step_next[k][n];
-                    X[n] = sum_value(xs[n][0], xs[n][1]);
+                    const float st = UP ? __uint_as_float(lds32_u32(sp[n] + 4u * (i / XBLK))) : step_next[k][n];
+                    const float x = -sum_value(xs[n][0], xs[n][1]);
+                    step[n] = pack2(st, st);
+                    X[n] = pack2(x, x);
                 }
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const uint2 sv = lds64_u32(sz + 64u * hf), zv = lds64_u32(sz + 64u * hf + sz_bytes / 2);
-                    const float2 s01 = T16::pair(sv.x), s23 = T16::pair(sv.y);
-                    const float2 z01 = T16::pair(zv.x), z23 = T16::pair(zv.y);
-                    const float sc[4] = {s01.x, s01.y, s23.x, s23.y};
-                    const float zc[4] = {z01.x, z01.y, z23.x, z23.y};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int T = 0; T < 2; ++T) {   // columns 2 T and 2 T + 1
+                        const float2 sf = T16::pair(T ? sv.y : sv.x), zf = T16::pair(T ? zv.y : zv.x);
+                        const uint64_t s2 = pack2(sf.x, sf.y), z2 = pack2(zf.x, zf.y);
 #pragma unroll
                         for (int n = 0; n < AT; ++n) {
-                            const int k = 2 * (c & 1);
-                            const float D = sum_value(d[hf][c >> 1][n][k], d[hf][c >> 1][n][k + 1]);
+                            const int(&v)[4] = d[hf][T][n];
+                            const uint64_t D = pack2(sum_value(v[0], v[1]), sum_value(v[2], v[3]));
                             // (s step first: the other product can pass fp32's range where the result does not)
-                            acc[hf][c][n] = fmaf(sc[c] * step[n], fmaf(-zc[c], X[n], D), acc[hf][c][n]);
+                            acc[hf][T][n] = fma2(mul2(s2, step[n]), fma2(z2, X[n], D), acc[hf][T][n]);
                         }
+                    }
                 }
             };
             int gleft = p.spg - q0 % p.spg;   // steps left in the current group
@@ -774,12 +807,10 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                             float* const row = mine + sl / p.top_k * TC + 4 * cg;
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
-                                float4 v = *reinterpret_cast<float4*>(row + 32 * hf);
-                                v.x = fmaf(a, acc[hf][0][n], v.x);
-                                v.y = fmaf(a, acc[hf][1][n], v.y);
-                                v.z = fmaf(a, acc[hf][2][n], v.z);
-                                v.w = fmaf(a, acc[hf][3][n], v.w);
-                                *reinterpret_cast<float4*>(row + 32 * hf) = v;
+                                ulonglong2 v = *reinterpret_cast<ulonglong2*>(row + 32 * hf);
+                                v.x = fma2(pack2(a, a), acc[hf][0][n], v.x);
+                                v.y = fma2(pack2(a, a), acc[hf][1][n], v.y);
+                                *reinterpret_cast<ulonglong2*>(row + 32 * hf) = v;
                             }
                         }
                         __syncwarp();
@@ -793,8 +824,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 if (pos < bm)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf)
-                        *reinterpret_cast<float4*>(red + (wk * p.bt + pos) * TC + MCOLS * wc + 32 * hf + 4 * cg) =
-                            make_float4(acc[hf][0][n], acc[hf][1][n], acc[hf][2][n], acc[hf][3][n]);
+                        *reinterpret_cast<ulonglong2*>(red + (wk * p.bt + pos) * TC + MCOLS * wc + 32 * hf + 4 * cg) =
+                            make_ulonglong2(acc[hf][0][n], acc[hf][1][n]);
             }
         };
         if (NT == 1 || bm <= 4) run(std::integral_constant<int, 1>{});
@@ -936,7 +967,6 @@ struct Cut {
     int W, WK, cluster;   // warps, warps along K, CTAs per column tile (DOWN)
     int xcol, nsteps, smem;
 };
-int warp_steps(int QC, int WK) { return ((QC + WK - 1) / WK + XBLK - 1) / XBLK * XBLK; }
 
 void cut_smem(Cut& c, bool up, int T, int S, int Q) {
     c.xcol = up ? xcol_bytes(Q) : 0;
@@ -950,25 +980,23 @@ void cut_smem(Cut& c, bool up, int T, int S, int Q) {
 //  * Few tokens, and no more tiles of 64 values of h than SMs: CTAs of 8 warps, beside which DOWN's start while
 //    they run (1 token, 8 experts of 2048 x 1024: 16.2 us against 19.7 us with 16 warps; with 344 tiles, 2 experts of
 //    4096 x 11008, 59 us against 45 us).
-//  * Else 16 warps: 4 along K, with tiles of 128 values, unless 8 leave fewer steps idle.  (8 with tiles of 64 also
-//    where that fills the SMs' last round better measured slower: DOWN's shorter fixed-point blocks cost more. 16
-//    tokens, 64 experts of 2048 x 1024: 96 us against 81 us.)
+//  * Else 16 warps and tiles of 128 values, 4 warps along K.  (8 along K and tiles of 64, where that fills the SMs'
+//    last round better, measured slower: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64 experts of 2048 x
+//    1024: 96 us against 81 us.)
 Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
-    const int Q = (K + SK - 1) / SK, sms = sm_count();
-    const long long slots = std::min(S, E), tiles = (I + 63) / 64;   // of 64 values
+    const int Q = (K + SK - 1) / SK;
     Cut c{};
     c.spg = group_size == -1 || group_size == K ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
     c.cluster = 1;
-    if (T <= 4 && tiles * slots <= sms) {
+    c.WK = 4;
+    if (T <= 4 && (long long)((I + 63) / 64) * std::min(S, E) <= sm_count()) {
         c.W = 8;
-        c.WK = 4;
         c.bt = 4;
         cut_smem(c, true, T, S, Q);
         if (c.smem <= max_smem(8)) return c;
     }
     c.W = 16;
-    c.WK = 8 * warp_steps(Q, 8) < 4 * warp_steps(Q, 4) ? 8 : 4;
     for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; --c.bt) {
         cut_smem(c, true, T, S, Q);
         if (c.smem <= max_smem(16)) break;
@@ -1027,7 +1055,7 @@ Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
             const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
             const int fit = std::max(1, few ? all / 2 : all);
             const int waves = (tiles + fit - 1) / fit, use = (int)(100ll * tiles * cs / ((long long)waves * places));
-            if (use > best + 2 || (few && use >= best && WK == 4)) {
+            if (use > best + 2) {
                 best = use;
                 c.WK = WK;
                 c.cluster = cs;
@@ -1062,11 +1090,9 @@ wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, b
     if (const wq_status st = ensure_smem_attr((const void*)kern, max_smem(W), attr_ctx, dev); st != WQ_OK) return st;
     // More blocks than these cannot be: each expert's last block may be short.
     const int blocks = std::min(p.S, std::min(p.E, p.S) + p.S / p.bt);
-    if ((long long)blocks * 5 * std::max(p.ntiles, (p.Q + XBLK - 1) / XBLK) >= 1ll << 31) return WQ_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
     const long long ctas = UP ? std::min<long long>(sm_count() * (16 / W), (long long)blocks * p.ntiles)
                               : (long long)p.ntiles * p.cluster;
-    if (ctas > 0x7fffffffll) return WQ_ERR_UNSUPPORTED;
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(W * 32, 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -1127,8 +1153,7 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
     using N16 = std::integral_constant<int, 16>;
     if constexpr (UP) {
         if (c.W == 8) return go(N1{}, N8{}, N4{});
-        if (c.bt <= 4) return c.WK == 4 ? go(N1{}, N16{}, N4{}) : go(N1{}, N16{}, N8{});
-        return c.WK == 4 ? go(N2{}, N16{}, N4{}) : go(N2{}, N16{}, N8{});
+        return c.bt <= 4 ? go(N1{}, N16{}, N4{}) : go(N2{}, N16{}, N4{});
     } else {
         if (c.bt <= 4) {
             if (c.WK == 1) return go(N1{}, N8{}, N1{});
@@ -1160,7 +1185,11 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
     const Cut up = last.up, down = last.down;
     p.Qh = (m.I + SK - 1) / SK;
     p.hb = MCOLS * (up.W / up.WK) / 2 / SK;   // a tile of UP: 128 values or 64
-    if (up.bt == 0 || down.bt == 0) return WQ_ERR_UNSUPPORTED;
+    // (before anything is launched: what must fit 31 bits -- the weighted line of work, word rows, CTAs)
+    const long long units = std::max((m.I + 31) / 32, (p.Qh + XBLK - 1) / XBLK), most = 1ll << 31;
+    if (up.bt == 0 || down.bt == 0 || p.S * 4 * units >= most || (long long)p.E * (m.K * BITS / 32) >= most ||
+        (long long)p.E * ((long long)m.I * BITS / 32) >= most || (m.N + 63ll) / 64 * 8 >= most)
+        return WQ_ERR_UNSUPPORTED;
     p.hq = static_cast<int8_t*>(m.ws);
     p.hstep = reinterpret_cast<float*>(p.hq + (size_t)2 * p.S * p.Qh * SK);
     p.NW = 2 * m.I;

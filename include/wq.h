@@ -413,8 +413,8 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  *   activation  WQ_ACT_SILU: g / (1 + exp(-g)); WQ_ACT_GELU: g * Phi(g), the exact form.
  *   workspace   wq_moe_workspace_size() bytes of device memory, 256-byte aligned,
  *            any contents; calls that may run at the same time must not share it.
- * The codes are multiplied as integers: x and h (fp32) become 16-bit fixed
- * point, with a power-of-two step per token and aligned block of 128 values
+ * The codes are multiplied as integers: x and h become 16-bit fixed
+ * point, with a power-of-two step per token and aligned block of at most 128 values
  * that puts the block's largest between 2^14 and 2^15 (error at most 2^-15 of
  * that value; none for values that end at or above the step).  Their products
  * are summed exactly over a block, blocks and slots in fp32, in an order that

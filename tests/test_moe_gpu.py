@@ -25,6 +25,14 @@ CASES = [
     (48, 32, 4, 256, 192, 128, 8, 32, "bf16", "silu", True),
     (64, 16, 16, 64, 32, 64, 4, 32, "fp16", "silu", False),      # 1024 slots, 64 tokens on every expert
     (64, 512, 2, 32, 32, 8, 4, 32, "bf16", "silu", False),       # as many experts as there can be
+    (3, 4, 2, 192, 96, 72, 4, 96, "fp16", "silu", True),         # groups of 3 steps, across stages
+    (6, 3, 2, 480, 320, 64, 4, 160, "bf16", "gelu", False),      # and of 5
+    (20, 4, 2, 192, 96, 72, 8, 96, "fp16", "silu", False),       # more tokens than the warps keep sums for
+    (15, 5, 4, 224, 32, 200, 4, 32, "bf16", "silu", False),
+    (40, 6, 3, 96, 352, 328, 4, -1, "fp16", "gelu", True),
+    (2, 2, 1, 64, 32, 20008, 4, 32, "fp16", "silu", False),      # a column tile per CTA: no cluster
+    (24, 3, 1, 32, 64, 12296, 8, 32, "bf16", "silu", False),
+    (4, 3, 2, 64, 2080, 136, 8, 32, "bf16", "gelu", False),
     (7, 3, 2, 8256, 32, 16, 4, 32, "bf16", "silu", False),       # a long K: two slots per block
     (2, 2, 1, 20000, 16, 8, 8, -1, "fp16", "silu", False),       # one slot per block
     (6, 2, 1, 64, 6176, 24, 4, 32, "fp16", "silu", True),        # a long inner length: K splits
