@@ -306,7 +306,7 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
 
 size_t wq_moe_workspace_size(int T, int top_k, int inner, int N) {
     if (T < 1 || T > WQ_MOE_MAX_TOKENS || top_k < 1 || top_k > 16 || inner < 1 || N < 1) return 0;
-    return wq::moe_workspace_bytes(T, top_k, inner);
+    return wq::moe_workspace_bytes(T, top_k, inner, N);
 }
 
 wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* w_up,

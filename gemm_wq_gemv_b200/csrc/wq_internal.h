@@ -93,7 +93,7 @@ struct MoeProblem {
     unsigned flags;
     void* ws;
 };
-size_t moe_workspace_bytes(int T, int top_k, int I);
+size_t moe_workspace_bytes(int T, int top_k, int I, int N);
 wq_status launch_moe(const MoeProblem& m, cudaStream_t s);
 wq_status moe_device_status(int reset);
 

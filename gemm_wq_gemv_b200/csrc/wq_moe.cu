@@ -14,16 +14,19 @@
 //    fewer when K is very long), so an expert's words are read once for them.  Every
 //    CTA derives the blocks from the ids.  UP (one CTA of 16 warps per SM): the
 //    (block, column tile) pairs, all of K each, are dealt out over the SMs in runs of
-//    equal weight.  DOWN (two CTAs of 8 warps per SM): a tile of 64 columns belongs to
-//    a cluster of up to 8 CTAs, among whose warps the tile's (block, part of K) line is
-//    dealt out; every warp sums y, weighted, in its own copy in shared memory, and the
-//    copies are joined at the end, across the cluster through distributed shared
-//    memory, in a fixed order.  (Rows per slot in global memory, summed by the last
-//    CTA to arrive, cost 1 us per item for the fence and up to 17 us at the end.)
-//    Where no copies fit (more than 16 tokens), and in UP, the warps split K or the
-//    tile's columns, 64 columns each (UP: 32 gate and the matching 32 up columns, so
-//    the activation needs no second pass), and their partials meet in shared memory
-//    while the loads of the next item run.
+//    equal weight; its warps split K and the tile's columns, 64 columns each (32 gate and
+//    the matching 32 up columns, so the activation needs no second pass), and their
+//    partials meet in shared memory while the loads of the next item run.  DOWN (two CTAs
+//    per SM): a tile of 64 columns belongs to a cluster of up to 8 CTAs, among whose warps
+//    the tile's (block, part of K) line is dealt out; a warp works alone on its run.  Up
+//    to 16 tokens every warp sums y, weighted, in its own copy in shared memory, and the
+//    copies are joined at the end, across the cluster through distributed shared memory.
+//    With more, the copies do not fit: a warp leaves the rows of its (block, part) in
+//    global memory (L2), and the cluster sums them at its end.  Both in a fixed order.
+//    (Measured: rows instead of copies, 16 tokens of 64 experts: 71 us against 64 us;
+//    instead of a split of K over the CTA's warps with two barriers per item, 32 tokens:
+//    85 us against 95 us; one copy per CTA with the warps adding in turn: 97 us; a last
+//    CTA to arrive that sums rows: 1 us per item for the fence and up to 17 us at the end.)
 //  * Products on integers.  Unpacking codes to fp16 or bf16 costs 7 instructions
 //    per word of 8 codes, and with m16n8k16 (2.1 clocks per SM on B200) that held
 //    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
@@ -77,12 +80,16 @@ namespace {
 
 constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
 constexpr int MAXBT = 8;        // slots per block
-constexpr int SOLO_T = 16;      // most tokens for which every warp of DOWN keeps sums of its own
+constexpr int SUMS_T = 16;      // most tokens for which every warp of DOWN keeps sums of y of its own
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
 constexpr int BOX_ROWS = 16;    // word rows per TMA box
 constexpr int STAGE = 2 * BOX_ROWS * 128;   // bytes: two halves
-constexpr int NST = 2;          // ring stages per warp
+constexpr int NST = 2;          // ring stages per warp (DOWN with 3: the same time)
+// Warps of a CTA of DOWN.  Two token tiles need 160 registers: with 8 warps of 128 the spilled ones passed through
+// L2, shared memory leaving little L1 (16 tokens, 2 of 8 experts: 139 us against 122 us; 48 tokens, 8-bit: 111 us
+// against 96 us).  With one token tile, 8 (1 token: 15.5 us against 18.9 us).
+constexpr int down_warps(int nt) { return nt == 1 ? 8 : 6; }
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int BITS> constexpr int step_rows() { return SK * BITS / 32; }   // word rows per step: 4 or 8
@@ -94,6 +101,7 @@ struct MoeParams {
     const int32_t* ids;     // (T, top_k)
     const float* weights;   // (T, top_k)
     uint16_t* y;            // (T, N)
+    float* rows;            // DOWN, many tokens: (tiles, S + bt * warps of a cluster, 64), the items' rows; else NULL
     int T, top_k, S, E, bt; // bt: slots per block
     int K;                  // inner length of this product (UP: K of x, DOWN: I)
     int NW;                 // weight columns (UP: 2 I, DOWN: N)
@@ -225,7 +233,7 @@ __device__ __forceinline__ void share_out(const Blocks& b, int units, int i, int
     }
 }
 
-// Fills the table and this CTA's share; every thread returns after both are complete.  cnt: scratch, E ints.
+// Fills the table and this CTA's share; every thread returns after both are complete.  cnt: scratch, E ints and S shorts.
 template <int MT>
 __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b, int* cnt, int units, int part,
                                             int parts) {
@@ -274,9 +282,12 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
     }
     for (int e = threadIdx.x; e < p.E; e += MT) cnt[e] = 0;
     __syncthreads();
+    int16_t* const of = reinterpret_cast<int16_t*>(cnt + p.E);   // the slots' experts
     for (int i = threadIdx.x; i < p.S; i += MT) {
         const int id = p.ids[i];
-        if (id >= 0 && id < p.E) atomicAdd(&cnt[id], 1);
+        const bool in = id >= 0 && id < p.E;
+        of[i] = in ? (int16_t)id : (int16_t)-1;
+        if (in) atomicAdd(&cnt[id], 1);
     }
     __syncthreads();
     if (warp == 0) {
@@ -326,8 +337,7 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
         __syncwarp();
         for (int i0 = 0; i0 < p.S; i0 += 32) {   // the slots in ascending order
             const int i = i0 + lane;
-            int id = i < p.S ? p.ids[i] : -1;
-            if (id >= p.E || id < 0) id = -1;
+            const int id = i < p.S ? of[i] : -1;
             const unsigned same = __match_any_sync(0xffffffffu, id < 0 ? -1 - lane : id);
             const int at = id < 0 ? 0 : cnt[id] + __popc(same & lt);
             __syncwarp();
@@ -386,9 +396,9 @@ __host__ __device__ constexpr int table_at(int W, int bt) { return W * bt * MCOL
 __host__ __device__ constexpr int values_at(int W, int bt, int S) { return table_at(W, bt) + table_bytes(S); }
 __host__ __device__ constexpr int steps_at(int W, int bt, int S, int xcol) { return values_at(W, bt, S) + 2 * bt * xcol; }
 
-// NT: token tiles of 4 slots (8 MMA columns).  MW: warps, WK of them along K.
-template <int BITS, bool BF, int NT, bool UP, int MW, int WK>
-__global__ void __launch_bounds__(MW * 32, 16 / MW)
+// NT: token tiles of 4 slots (8 MMA columns).  MW: warps.
+template <int BITS, bool BF, int NT, bool UP, int MW>
+__global__ void __launch_bounds__(MW * 32, UP ? 16 / MW : 2)
 moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_s,
            const __grid_constant__ CUtensorMap tm_z, const MoeParams p) {
     constexpr int MT = MW * 32;
@@ -396,26 +406,25 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     constexpr int RPS = step_rows<BITS>();       // 4 or 8
     constexpr int RL = RPS / 4;                  // word rows per lane and step
     constexpr int SPS = BOX_ROWS / RPS;          // steps per stage
-    // DOWN with WK = 1: every warp works alone, on the tile's 64 columns and its own share of the (block, K) line,
-    // and sums y in its own copy: no barrier until the end.
-    constexpr bool SOLO = !UP && WK == 1;
-    constexpr int WC = SOLO ? 1 : MW / WK;       // warps along the columns
+    constexpr int WK = UP ? 4 : 1;               // UP: warps along K
+    constexpr int WC = UP ? MW / WK : 1;         // and along the columns.  DOWN: every warp works alone
     constexpr int TC = MCOLS * WC;               // weight columns per tile
     extern __shared__ uint8_t smem_raw[];
     // the 128-byte swizzle of the TMA boxes repeats every 1024 bytes
     uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     __shared__ Head head;
-    __shared__ uint64_t bars[MW * NST];
+    __shared__ uint64_t bars[MW * NST], free_bar;   // free_bar (UP): the partials have been read
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     // 16-byte column chunk of this lane (columns 4 cg .. 4 cg + 3 of each half): with the lines of a
     // stage below, the eight lanes of a quarter-warp meet eight different bank groups
     const int cg = UP ? g : ((g & 1) << 2) | (g >> 1);
-    const int wk = SOLO ? 0 : warp / WC, wc = warp % WC;
+    const int wk = warp / WC, wc = warp % WC;   // UP
     uint64_t* const bar = bars + warp * NST;
     if (lane == 0) {
         for (int i = 0; i < NST; ++i) mbar_init(&bar[i], 1);
+        if (UP && warp == 0) mbar_init(&free_bar, MW);
         fence_mbarrier_init();
         if (warp == 1) prefetch_tmap(&tm);
         if (warp == 2) prefetch_tmap(&tm_s);
@@ -427,7 +436,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const int rank = UP ? 0 : (int)blockIdx.x % p.cluster;
     const uint32_t sz_bytes = 256u * (uint32_t)p.sz_rows;   // a stage's s rows, then its z rows
     const uint32_t roff = MW * NST * (STAGE + sz_bytes);    // behind the rings
-    constexpr int RW = SOLO ? 0 : MW;   // warps with partials in shared memory
+    constexpr int RW = UP ? MW : 0;   // warps with partials in shared memory
     uint8_t* const tab = smem + roff + table_at(RW, p.bt);
     const int ts = table_slots(p.S);
     int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
@@ -435,117 +444,128 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     if constexpr (UP) find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), p.ntiles, blockIdx.x, gridDim.x);
     else find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), Q4, rank, p.cluster);
     int at0 = head.i0, end = head.i1;
-    if constexpr (SOLO) {
+    if constexpr (!UP) {   // this warp's
         at0 = end = 0;
         if (head.n > 0) {
             at0 = share(blk, Q4, rank * MW + warp, p.cluster * MW);
             end = share(blk, Q4, rank * MW + warp + 1, p.cluster * MW);
         }
     }
-    // ---- this CTA's items.  UP: (block, tile) pairs, all steps of K; DOWN: one tile, runs of a block's steps.
+    // ---- the items.  UP, the CTA's: (block, tile) pairs, all steps of K; DOWN, the warp's: one tile, runs of a block's steps.
     struct Item {
-        int at, u, tile, s0, ns;   // position on the line, block, column tile, first step, steps
+        int at, u, tile, s0, ns;   // position on the line, block, column tile; this warp's first step and steps
     };
-    auto open = [&](Item& it) {    // the item at it.at
+    Item it;                       // (divisions here alone, none per item)
+    it.at = at0;
+    it.u = at0 / (UP ? p.ntiles : Q4);
+    if constexpr (UP) {            // the warps along K: whole fixed-point blocks
+        it.tile = at0 - it.u * p.ntiles;
+        const int per = ((p.Q + WK - 1) / WK + XBLK - 1) / XBLK * XBLK;
+        it.s0 = min(p.Q, wk * per);
+        it.ns = min(p.Q, it.s0 + per) - it.s0;
+    } else {
+        it.tile = (int)blockIdx.x / p.cluster;
+        it.s0 = (at0 - it.u * Q4) * XBLK;
+        it.ns = min(p.Q - it.s0, (end - at0) * XBLK);
+    }
+    auto next = [&](Item& it) {
         if constexpr (UP) {
-            it.u = it.at / p.ntiles;
-            it.tile = it.at - it.u * p.ntiles;
-            it.s0 = 0;
-            it.ns = p.Q;
+            ++it.at;
+            if (++it.tile == p.ntiles) {
+                it.tile = 0;
+                ++it.u;
+            }
         } else {
-            it.u = it.at / Q4;
-            const int b4 = it.at - it.u * Q4;
-            it.tile = (int)blockIdx.x / p.cluster;
-            it.s0 = b4 * XBLK;
-            it.ns = min(p.Q - it.s0, (end - it.at) * XBLK);
+            it.at += (it.ns + XBLK - 1) / XBLK;
+            ++it.u;
+            it.s0 = 0;
+            it.ns = min(p.Q, (end - it.at) * XBLK);
         }
-    };
-    auto next = [&](Item& it) { it.at += UP ? 1 : (it.ns + XBLK - 1) / XBLK; };
-    // steps of this warp in an item: [first, first + count), whole fixed-point blocks
-    auto range = [&](const Item& it, int& first) {
-        if constexpr (SOLO) {
-            first = it.s0;
-            return it.ns;
-        }
-        const int per = ((it.ns + WK - 1) / WK + XBLK - 1) / XBLK * XBLK;
-        first = min(it.ns, wk * per);
-        const int n = min(it.ns, first + per) - first;
-        first += it.s0;
-        return n;
     };
     // first column of this warp in a tile (UP: of the gate; the up columns are the map's second plane)
-    auto col = [&](int tile) { return UP ? tile * (TC / 2) + 32 * wc : tile * TC + MCOLS * wc; };
+    auto col = [&](int tile) { return UP ? tile * (TC / 2) + 32 * wc : tile * TC; };
     // ---- loads: a cursor over the (item, stage) sequence of this warp
     const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (NST * STAGE);
     const uint32_t sz_ring = smem_u32(smem) + MW * NST * STAGE + (uint32_t)warp * (NST * sz_bytes);
-    Item wit;
-    wit.at = at0;
-    int wq = 0, wleft = 0, wslot = 0;   // next step, stages left in the item, ring slot
-    bool ok = true, wopen = false;
-    auto issue = [&]() {
-        while (wleft == 0) {
-            if (wopen) next(wit);
-            wopen = wit.at < end;
-            if (!wopen) return;
-            open(wit);
-            wleft = (range(wit, wq) + SPS - 1) / SPS;
+    Item wit = it;                          // the item whose stages are being requested
+    const int g0 = it.s0 / p.spg, gp0 = it.s0 - g0 * p.spg;   // UP: of every item; DOWN: of the first, then 0
+    int wleft = 0;                          // stages left in it
+    int row = 0, grow = 0, gpos = 0;        // the next stage: word row, s row, steps into its group
+    bool ok = true, first = true;
+    auto issue = [&](uint32_t slot) {
+        if (wleft == 0) {
+            // (an item of UP has no steps for a warp past the end of K: nor has any other)
+            if (!first) next(wit);
+            if (wit.at >= end || wit.ns == 0) return;
+            wleft = (wit.ns + SPS - 1) / SPS;
+            const int e = blk.e[wit.u];
+            row = e * p.Kw + wit.s0 * RPS;
+            grow = e * p.groups + (UP || first ? g0 : 0);
+            gpos = UP || first ? gp0 : 0;
+            first = false;
         }
         if (lane == 0) {
-            mbar_arrive_expect_tx(&bar[wslot], STAGE + sz_bytes);
-            const uint32_t dst = ring + (uint32_t)wslot * STAGE, sz = sz_ring + (uint32_t)wslot * sz_bytes;
-            const int e = blk.e[wit.u], row = e * p.Kw + wq * RPS, grow = e * p.groups + wq / p.spg;
-            const int c = col(wit.tile);
+            uint64_t* const b = &bar[slot];
+            mbar_arrive_expect_tx(b, STAGE + sz_bytes);
+            const int wcol = col(wit.tile);
+            const uint32_t dst = ring + slot * STAGE, sz = sz_ring + slot * sz_bytes;
             if constexpr (UP) {
-                tma_load_3d_u32(dst, &tm, &bar[wslot], c, 0, row);
-                tma_load_3d_u32(sz, &tm_s, &bar[wslot], c, 0, grow);
-                tma_load_3d_u32(sz + sz_bytes / 2, &tm_z, &bar[wslot], c, 0, grow);
+                tma_load_3d_u32(dst, &tm, b, wcol, 0, row);
+                tma_load_3d_u32(sz, &tm_s, b, wcol, 0, grow);
+                tma_load_3d_u32(sz + sz_bytes / 2, &tm_z, b, wcol, 0, grow);
             } else {
-                tma_load_2d_u32(dst, &tm, &bar[wslot], c, row);
-                tma_load_2d_u32(dst + STAGE / 2, &tm, &bar[wslot], c + 32, row);
-                tma_load_2d_u32(sz, &tm_s, &bar[wslot], c, grow);
-                tma_load_2d_u32(sz + sz_bytes / 2, &tm_z, &bar[wslot], c, grow);
+                tma_load_2d_u32(dst, &tm, b, wcol, row);
+                tma_load_2d_u32(dst + STAGE / 2, &tm, b, wcol + 32, row);
+                tma_load_2d_u32(sz, &tm_s, b, wcol, grow);
+                tma_load_2d_u32(sz + sz_bytes / 2, &tm_z, b, wcol, grow);
             }
         }
-        wq += SPS;
+        row += BOX_ROWS;
+        for (gpos += SPS; gpos >= p.spg; gpos -= p.spg) ++grow;
         --wleft;
-        wslot ^= 1;
     };
-    issue();
-    issue();
+    issue(0);
+    issue(1);
 
     if constexpr (!UP) grid_dependency_wait();   // h
     float* const red = reinterpret_cast<float*>(smem + roff);   // [wk][slot][TC]
     const uint32_t xoff = roff + values_at(RW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
     float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));         // UP: [slot][block]
-    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [T][TC], SOLO: one per warp
+    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [warp][T][TC]
     // This lane's 16-byte vectors of word row t (and t + 4): line r of 128 bytes holds them at chunk
     // cg ^ (r & 7).  UP: the lines of a word row's two halves follow each other; DOWN: 16 lines each.
     constexpr uint32_t HALF = UP ? 128u : STAGE / 2, LINE = UP ? 256u : 128u;   // to the other half, to the next row
-    auto vec = [&](int r, int hf) {
-        const uint32_t line = UP ? 2 * r + hf : r;
-        return (uint32_t)r * LINE + (uint32_t)hf * HALF + (((uint32_t)cg ^ (line & 7u)) << 4);
+    // (UP: rows 4 apart have the same swizzle; DOWN: the two halves have)
+    const uint32_t off0 = t * LINE + (((uint32_t)cg ^ ((UP ? 2 * t : t) & 7u)) << 4);
+    const uint32_t off1 = UP ? t * LINE + HALF + (((uint32_t)cg ^ ((2 * t + 1) & 7u)) << 4)
+                             : (t + 4) * LINE + (((uint32_t)cg ^ (t + 4u)) << 4);
+    auto off = [&](int odd, int hf) {   // constants
+        if constexpr (UP) return (hf ? off1 : off0) + 4 * LINE * odd;
+        else return (odd ? off1 : off0) + HALF * hf;
     };
-    // word rows t and t + 4, halves 0 and 1 (UP: rows 4 apart have the same swizzle)
-    const uint32_t off[2][2] = {{vec(t, 0), vec(t, 1)}, {vec(t + 4, 0), vec(t + 4, 1)}};
-    int rslot = 0, phase = 0;   // ring position of the next stage to read
+    uint32_t slot = 0, phase = 0;   // ring position of the next stage to read
+    auto advance = [&]() {
+        slot ^= 1u;
+        phase ^= slot ^ 1u;
+    };
 
     if constexpr (!UP)
-        for (int i = threadIdx.x; i < p.T * TC * (SOLO ? MW : 1); i += MT) ys[i] = 0.0f;
-    if constexpr (SOLO) __syncthreads();   // (elsewhere a barrier precedes their first use)
+        if (p.rows == nullptr) {
+            for (int i = lane; i < p.T * TC; i += 32) ys[warp * p.T * TC + i] = 0.0f;
+            __syncwarp();
+        }
 
     int block = -1;   // UP: the block whose values are in shared memory
-    Item it;
-    for (it.at = at0; it.at < end; next(it)) {
-        open(it);
-        int q0;
-        const int nq = range(it, q0);
+    int done = 0;     // items finished
+    for (; it.at < end; next(it)) {
+        const int q0 = it.s0, nq = it.ns;
         const int16_t* const slots = blk.order + blk.first[it.u];
         const int bm = blk.count(it.u);
         if (UP && it.u != block) {
             // ---- another block: x of its slots as fixed point.  Column 2 m holds hi of the block's slot m, 2 m + 1
             // its lo: 32 bytes per step, 8 for each word row t.
             block = it.u;
-            __syncthreads();   // the previous block's values are no longer read
+            // (the previous block's were last read before the barrier behind the partials)
             // (slot, 8 steps) pairs of this warp, XU at a time so that their loads overlap; a lane has 8 values
             const int rounds = (nq + 7) / 8, pairs = bm > wc ? (bm - wc + WC - 1) / WC * rounds : 0;
             constexpr int XU = 4;
@@ -590,8 +610,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                     const uint32_t E = block_exponent(top);
                     uint2 hi, lo;
                     to_fixed<BITS>(v, __uint_as_float((268u - E) << 23), hi, lo);
-                    const uint32_t at = xbase + (uint32_t)(2 * m) * p.xcol + (uint32_t)(q - it.s0) * 32u;
-                    if (in && check((q - it.s0) * 32 + 32 <= p.xcol, &g_moe_status)) {
+                    const uint32_t at = xbase + (uint32_t)(2 * m) * p.xcol + (uint32_t)q * 32u;
+                    if (in && check(q * 32 + 32 <= p.xcol, &g_moe_status)) {
                         if constexpr (BITS == 4) {
                             sts64(at + 8u * t, hi.x, hi.y);
                             sts64(at + p.xcol + 8u * t, lo.x, lo.y);
@@ -603,8 +623,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                             sts32(at + p.xcol + o + 8u, lo.y);
                         }
                     }
-                    if ((lane & 15) == 0 && in && check((q - it.s0) / XBLK < p.nsteps, &g_moe_status))
-                        steps[m * p.nsteps + (q - it.s0) / XBLK] = block_step(top, E);
+                    if ((lane & 15) == 0 && in && check(q / XBLK < p.nsteps, &g_moe_status))
+                        steps[m * p.nsteps + q / XBLK] = block_step(top, E);
                 }
             }
             __syncthreads();
@@ -621,20 +641,24 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             // B column g of token tile n: UP from shared memory; DOWN straight from global memory, a stage ahead (every
             // CTA reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
             uint32_t xa[AT], sp[AT];               // UP
-            const int8_t* hp[AT];                  // DOWN: values and steps
-            const float* hs[AT];
+            uint32_t hp[AT], hs[AT];               // DOWN: values and steps (below 2^31: checked by the host)
             uint2 bx[SPS][AT];
             float step_next[2][AT];
+            [[maybe_unused]] float wt[AT];         // DOWN: weights of the slots 4 n + t and their rows of y's sums
+            [[maybe_unused]] uint32_t yrow[AT];
             const int xb = UP ? XBLK : p.hb;       // steps per fixed-point block: XBLK, or 2
 #pragma unroll
             for (int n = 0; n < AT; ++n) {
                 if constexpr (UP) {
-                    xa[n] = xoff + (uint32_t)min(8 * n + g, 2 * p.bt - 1) * p.xcol + (uint32_t)(q0 - it.s0) * 32u + 8u * t;
-                    sp[n] = smem_u32(steps + min(4 * n + t, p.bt - 1) * p.nsteps + (q0 - it.s0) / XBLK);
+                    xa[n] = xoff + (uint32_t)min(8 * n + g, 2 * p.bt - 1) * p.xcol + (uint32_t)q0 * 32u + 8u * t;
+                    sp[n] = smem_u32(steps + min(4 * n + t, p.bt - 1) * p.nsteps + q0 / XBLK);
                 } else {
                     const int col = 2 * slots[min(4 * n + (g >> 1), bm - 1)] + (g & 1);
-                    hp[n] = p.hq + ((size_t)col * p.Qh + q0) * SK + 8 * t;
-                    hs[n] = p.hstep + (size_t)slots[min(4 * n + t, bm - 1)] * p.Qh + q0 / p.hb;
+                    hp[n] = (uint32_t)(col * p.Qh + q0) * SK + 8 * t;
+                    const int sl = slots[min(4 * n + t, bm - 1)];
+                    hs[n] = sl * p.Qh + q0 / xb;
+                    wt[n] = p.weights[sl];
+                    yrow[n] = (uint32_t)(warp * p.T + sl / p.top_k) * TC + 4 * cg;
                     check(col < 2 * p.S, &g_moe_status);
                 }
             }
@@ -643,9 +667,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 for (int n = 0; n < AT; ++n) {
 #pragma unroll
                     for (int j = 0; j < SPS; ++j)
-                        if (i + j < nq) bx[j][n] = *reinterpret_cast<const uint2*>(hp[n] + (size_t)(i + j) * SK);
-                    if (i < nq) step_next[0][n] = hs[n][i / xb];
-                    if (SPS == 4 && xb == 2 && i + 2 < nq) step_next[1][n] = hs[n][i / xb + 1];
+                        if (i + j < nq) bx[j][n] = *reinterpret_cast<const uint2*>(p.hq + hp[n] + (uint32_t)((i + j) * SK));
+                    if (i < nq) step_next[0][n] = p.hstep[hs[n] + i / xb];
+                    if (SPS == 4 && xb == 2 && i + 2 < nq) step_next[1][n] = p.hstep[hs[n] + i / xb + 1];
                 }
             };
             if constexpr (!UP) request(0);
@@ -680,7 +704,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
 #pragma unroll
                     for (int r = 0; r < RL; ++r) {   // rows 4 j + t (4-bit), 8 j + t and 8 j + t + 4 (8-bit)
                         const int row8 = BITS == 4 ? j >> 1 : j, odd = BITS == 4 ? j & 1 : r;
-                        w[r][hf] = *reinterpret_cast<const uint4*>(st + off[odd][hf] + 8 * LINE * row8);
+                        w[r][hf] = *reinterpret_cast<const uint4*>(st + off(odd, hf) + 8 * LINE * row8);
                     }
 #pragma unroll
                 for (int n = 0; n < AT; ++n)
@@ -743,13 +767,13 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
 #pragma unroll 1
             for (int i = 0; i < nq; i += SPS) {
                 if (ok) {
-                    const bool good = mbar_wait_bounded(&bar[rslot], (uint32_t)phase, WAIT_NS);
+                    const bool good = mbar_wait_bounded(&bar[slot], phase, WAIT_NS);
                     if (!good) atomicOr(&g_moe_status, 1u);
                     ok = __all_sync(0xffffffffu, good);
                 }
                 if (!ok) break;
-                const uint8_t* const st = smem + (uint32_t)(warp * NST + rslot) * STAGE;
-                uint32_t sz = sz_ring + (uint32_t)rslot * sz_bytes + 8u * cg;   // the stage's first group
+                const uint8_t* const st = smem + (warp * NST + slot) * STAGE;
+                uint32_t sz = sz_ring + slot * sz_bytes + 8u * cg;   // the stage's first group
                 const uint8_t* xi[AT];
 #pragma unroll
                 for (int n = 0; n < AT; ++n) xi[n] = UP ? smem + xa[n] + 32u * i : nullptr;
@@ -788,28 +812,36 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 if constexpr (!UP) request(i + SPS);
                 __syncwarp();   // every lane has read the stage: refill it
                 fence_proxy_async_smem();
-                issue();
-                rslot ^= 1;
-                phase ^= rslot == 0;
+                issue(slot);
+                advance();
             }
-            if constexpr (SOLO) {
+            if constexpr (!UP) {
+                if (p.rows != nullptr) {   // the rows of this (warp, block), to be summed at the end
+                    float* const to = p.rows + ((size_t)it.tile * (p.S + p.bt * MW * p.cluster) + blk.first[it.u] +
+                                                p.bt * (rank * MW + warp)) * TC + 4 * cg;
+#pragma unroll
+                    for (int n = 0; n < AT; ++n)
+                        if (const int pos = 4 * n + t; pos < bm)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf)
+                                *reinterpret_cast<ulonglong2*>(to + pos * TC + 32 * hf) =
+                                    make_ulonglong2(acc[hf][0][n], acc[hf][1][n]);
+                    return;
+                }
                 // y += weight * row, in the warp's own sums; slots that share a token lie in different lanes t or n,
                 // which take turns
-                float* const mine = ys + warp * p.T * TC;
 #pragma unroll
                 for (int n = 0; n < AT; ++n)
 #pragma unroll 1
-                    for (int turn = 0; turn < 4; ++turn) {
-                        const int pos = 4 * n + turn;
-                        if (pos < bm && t == turn) {
-                            const int sl = slots[pos];
-                            const float a = p.weights[sl];
-                            float* const row = mine + sl / p.top_k * TC + 4 * cg;
+                    for (int tt = 0; tt < 4; ++tt) {
+                        if (4 * n + tt < bm && t == tt) {
+                            float* const row = ys + yrow[n];
+                            const uint64_t a = pack2(wt[n], wt[n]);
 #pragma unroll
                             for (int hf = 0; hf < 2; ++hf) {
                                 ulonglong2 v = *reinterpret_cast<ulonglong2*>(row + 32 * hf);
-                                v.x = fma2(pack2(a, a), acc[hf][0][n], v.x);
-                                v.y = fma2(pack2(a, a), acc[hf][1][n], v.y);
+                                v.x = fma2(a, acc[hf][0][n], v.x);
+                                v.y = fma2(a, acc[hf][1][n], v.y);
                                 *reinterpret_cast<ulonglong2*>(row + 32 * hf) = v;
                             }
                         }
@@ -817,7 +849,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                     }
                 return;
             }
-            // ---- the warps' partials meet in shared memory
+            // ---- the warps' partials meet in shared memory, once every warp has read the last item's
+            if (ok && done > 0) {
+                const bool good = mbar_wait_bounded(&free_bar, (uint32_t)(done - 1) & 1u, WAIT_NS);
+                if (!good) atomicOr(&g_moe_status, 1u);
+                ok = __all_sync(0xffffffffu, good);
+            }
 #pragma unroll
             for (int n = 0; n < AT; ++n) {
                 const int pos = 4 * n + t;
@@ -830,13 +867,13 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         };
         if (NT == 1 || bm <= 4) run(std::integral_constant<int, 1>{});
         else run(std::integral_constant<int, NT>{});
-        if constexpr (SOLO) continue;
-        __syncthreads();
         if constexpr (UP) {
+            __syncthreads();
             // The tile's TC / 2 values of h of one slot are one fixed-point block (128 or 64): LPS lanes, 4 each
             constexpr int LPS = TC / 8, SPW = 32 / LPS;
             const int c = 4 * (lane % LPS), cc = it.tile * (TC / 2) + c;
-            for (int pos0 = warp * SPW; pos0 < bm; pos0 += MW * SPW) {
+            // (by the warps in turn: the others go on to the next item)
+            for (int pos0 = (warp + MW / 2 * done) % MW * SPW; pos0 < bm; pos0 += MW * SPW) {
                 const int pos = min(pos0 + lane / LPS, bm - 1);
                 const bool mine = pos0 + lane / LPS < bm;
                 const float* const src = red + pos * TC + MCOLS * (c / 32) + c % 32;   // gate; its up column 32 on
@@ -880,70 +917,114 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 }
                 if (in && lane % LPS == 0) p.hstep[(size_t)slot * p.Qh + q / (TC / 2 / SK)] = block_step(top, E);
             }
-            __syncthreads();   // the partials are read: the next item may write its own
-        } else {
-            // y += weight * row: a thread takes one column of the tokens t = its group mod MT / TC, so two slots
-            // of one token meet in one thread
-            const int c = threadIdx.x % TC, grp = threadIdx.x / TC;
-            auto total = [&](int o) {   // over the warps along K, in their order
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WK; ++w) v += red[w * p.bt * TC + o];
-                return v;
-            };
-            for (int pos = 0; pos < bm; ++pos) {
-                const int sl = slots[pos], tok = sl / p.top_k;
-                if (tok % (MT / TC) == grp) ys[tok * TC + c] = fmaf(p.weights[sl], total(pos * TC + c), ys[tok * TC + c]);
-            }
-            __syncthreads();   // the partials are read: the next item may write its own
+            ++done;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&free_bar);
         }
     }
     if (!ok)   // gave up a wait: give the copies still in flight as long again
         for (int i = 0; i < NST; ++i) {
-            mbar_wait_bounded(&bar[rslot], (uint32_t)phase, WAIT_NS);
-            rslot ^= 1;
-            phase ^= rslot == 0;
+            mbar_wait_bounded(&bar[slot], phase, WAIT_NS);
+            advance();
         }
     if constexpr (!UP) {
-        // ---- the tile's CTAs join their sums, in their order; each writes its share of the rows
-        if constexpr (SOLO) {   // first the warps', in theirs
-            __syncthreads();
-            for (int i = threadIdx.x; i < p.T * (TC / 4); i += MT) {
-                float4 v = *reinterpret_cast<const float4*>(ys + 4 * i);
-#pragma unroll
-                for (int w = 1; w < MW; ++w) {
-                    const float4 o = *reinterpret_cast<const float4*>(ys + w * p.T * TC + 4 * i);
-                    v.x += o.x;
-                    v.y += o.y;
-                    v.z += o.z;
-                    v.w += o.w;
-                }
-                *reinterpret_cast<float4*>(ys + 4 * i) = v;
-            }
-        }
-        if (p.cluster > 1) cluster_sync();
-        else __syncthreads();
         const int tl = (int)blockIdx.x / p.cluster;
-        const uint32_t at = smem_u32(ys);
-        for (int i = rank + p.cluster * (int)threadIdx.x; i < p.T * (TC / 4); i += p.cluster * MT) {
-            const int tok = i / (TC / 4), cc = tl * TC + 4 * (i % (TC / 4));
-            if (cc >= p.NW) continue;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (p.cluster == 1) {
-                v = *reinterpret_cast<const float4*>(ys + 4 * i);
-            } else {
-                for (int r = 0; r < p.cluster; ++r) {
-                    const float4 o = ld_cluster_f4(map_shared_rank(at + 16u * i, r));
-                    v.x += o.x;
-                    v.y += o.y;
-                    v.z += o.z;
-                    v.w += o.w;
-                }
-            }
+        auto write = [&](int tok, int c, float4 v) {   // y[tok], columns c to c + 3 of the tile
+            const int cc = tl * TC + c;
+            if (cc >= p.NW) return;                    // N is a multiple of 4
             uint2 o;
             o.x = (uint32_t)T16::store(v.x) | ((uint32_t)T16::store(v.y) << 16);
             o.y = (uint32_t)T16::store(v.z) | ((uint32_t)T16::store(v.w) << 16);
             *reinterpret_cast<uint2*>(p.y + (size_t)tok * p.NW + cc) = o;
+        };
+        auto add = [](float4& v, const float4& o) {
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+        };
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p.rows != nullptr) {
+            // ---- the tile's rows are complete: every CTA sums those of its tokens (rank, rank + cluster, ..)
+            if (p.cluster > 1) cluster_sync();
+            else __syncthreads();
+            // in the rings' place: where each warp's run starts; per slot its place in `order` and its block's warps
+            const int nw = p.cluster * MW, ns = p.S + p.bt * nw;
+            int* const starts = reinterpret_cast<int*>(smem);                        // nw + 1
+            int16_t* const place = reinterpret_cast<int16_t*>(starts + 8 * MW + 1);  // S; then the first and the last warp
+            int16_t* const wfirst = place + p.S;
+            int16_t* const wlast = wfirst + p.S;
+            float* const part = reinterpret_cast<float*>(smem + 8192);               // [slots of a few tokens][TC]
+            constexpr int PART_ROWS = 192;
+            for (int i = threadIdx.x; i < p.S; i += MT) place[i] = -1;
+            for (int w = warp; w <= nw; w += MW) {
+                const int v = head.n > 0 ? share(blk, Q4, w, nw) : 0;
+                if (lane == 0) starts[w] = v;
+            }
+            __syncthreads();
+            for (int u = threadIdx.x; u < head.n; u += MT) {
+                int w0 = 0, w1 = nw;
+                while (w0 < nw - 1 && starts[w0 + 1] <= u * Q4) ++w0;
+                while (w1 > w0 + 1 && starts[w1 - 1] >= (u + 1) * Q4) --w1;
+                for (int i = blk.first[u]; i < blk.first[u + 1]; ++i) {
+                    place[blk.order[i]] = (int16_t)i;
+                    wfirst[blk.order[i]] = (int16_t)w0;
+                    wlast[blk.order[i]] = (int16_t)w1;
+                }
+            }
+            __syncthreads();
+            const int step = PART_ROWS / p.top_k;   // tokens at a time
+            for (int k0 = 0; rank + k0 * p.cluster < p.T; k0 += step) {
+                const int nt = min(step, (p.T - rank - k0 * p.cluster + p.cluster - 1) / p.cluster);
+                for (int i = threadIdx.x; i < nt * p.top_k * (TC / 4); i += MT) {
+                    const int r = i / (TC / 4), c = 4 * (i % (TC / 4));
+                    const int sl = (rank + (k0 + r / p.top_k) * p.cluster) * p.top_k + r % p.top_k;
+                    float4 v = zero;
+                    if (place[sl] >= 0 && check(sl < p.S, &g_moe_status)) {
+                        const float a = p.weights[sl];
+                        const float* const from = p.rows + ((size_t)tl * ns + place[sl]) * TC + c;
+                        for (int w = wfirst[sl]; w < wlast[sl]; w += 2) {   // (a run may be empty)
+                            float4 o0 = zero, o1 = zero;
+                            if (starts[w] < starts[w + 1])
+                                o0 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)p.bt * w * TC));
+                            if (w + 1 < wlast[sl] && starts[w + 1] < starts[w + 2])
+                                o1 = __ldcg(reinterpret_cast<const float4*>(from + (size_t)p.bt * (w + 1) * TC));
+                            add(v, o0);
+                            add(v, o1);
+                        }
+                        v = make_float4(a * v.x, a * v.y, a * v.z, a * v.w);
+                    }
+                    *reinterpret_cast<float4*>(part + 4 * i) = v;
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i < nt * (TC / 4); i += MT) {
+                    const int k = i / (TC / 4), c = 4 * (i % (TC / 4));
+                    float4 v = zero;
+                    for (int j = 0; j < p.top_k; ++j)
+                        add(v, *reinterpret_cast<const float4*>(part + (k * p.top_k + j) * TC + c));
+                    write(rank + (k0 + k) * p.cluster, c, v);
+                }
+                __syncthreads();
+            }
+            return;
+        }
+        // ---- the warps join their sums, then the tile's CTAs, each in their order; each CTA writes its share of the rows
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.T * (TC / 4); i += MT) {
+            float4 v = *reinterpret_cast<const float4*>(ys + 4 * i);
+#pragma unroll
+            for (int w = 1; w < MW; ++w) add(v, *reinterpret_cast<const float4*>(ys + w * p.T * TC + 4 * i));
+            *reinterpret_cast<float4*>(ys + 4 * i) = v;
+        }
+        if (p.cluster > 1) cluster_sync();
+        else __syncthreads();
+        const uint32_t at = smem_u32(ys);
+        for (int i = rank + p.cluster * (int)threadIdx.x; i < p.T * (TC / 4); i += p.cluster * MT) {
+            float4 v = zero;
+            if (p.cluster == 1) v = *reinterpret_cast<const float4*>(ys + 4 * i);
+            else
+                for (int r = 0; r < p.cluster; ++r) add(v, ld_cluster_f4(map_shared_rank(at + 16u * i, r)));
+            write(i / (TC / 4), 4 * (i % (TC / 4)), v);
         }
         __syncwarp();
         if (p.cluster > 1) cluster_sync();   // peers keep their shared memory until every read is done
@@ -964,7 +1045,8 @@ int xcol_bytes(int steps) {   // 32 mod 128: the four columns of a load phase li
 struct Cut {
     int spg, sz_rows;     // steps per group, s rows per stage
     int bt;               // slots per block
-    int W, WK, cluster;   // warps, warps along K, CTAs per column tile (DOWN)
+    int W, cluster;       // warps; CTAs per column tile (DOWN)
+    bool rows;            // DOWN: rows in global memory instead of the warps' own sums
     int xcol, nsteps, smem;
 };
 
@@ -972,7 +1054,7 @@ void cut_smem(Cut& c, bool up, int T, int S, int Q) {
     c.xcol = up ? xcol_bytes(Q) : 0;
     c.nsteps = up ? (Q + XBLK - 1) / XBLK : 0;
     c.smem = ring_bytes(c.W, c.sz_rows) + (up ? steps_at(c.W, c.bt, S, c.xcol) + c.bt * c.nsteps * 4
-                                              : values_at(c.WK == 1 ? 0 : c.W, c.bt, S) + T * MCOLS * (c.W / c.WK) * 4);
+                                              : values_at(0, c.bt, S) + (c.rows ? 0 : c.W * T * MCOLS * 4));
 }
 
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
@@ -989,7 +1071,6 @@ Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
     c.spg = group_size == -1 || group_size == K ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
     c.cluster = 1;
-    c.WK = 4;
     if (T <= 4 && (long long)((I + 63) / 64) * std::min(S, E) <= sm_count()) {
         c.W = 8;
         c.bt = 4;
@@ -1014,10 +1095,10 @@ int clusters_that_fit(int cs) {
     if (n > 0) return n;
     n = 2 * sm_count() / cs;
     if (cs > 1) {
-        auto kern = moe_kernel<4, false, 1, false, 8, 8>;
+        auto kern = moe_kernel<4, false, 1, false, down_warps(1)>;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(cs, 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
+        cfg.blockDim = dim3(down_warps(1) * 32, 1, 1);
         cfg.dynamicSmemBytes = max_smem(8);
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -1043,47 +1124,33 @@ int clusters_that_fit(int cs) {
 Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
     const int places = few ? sm_count() : 2 * sm_count();
     Cut c{};
-    c.W = 8;
+    c.W = down_warps(T <= 4 ? 1 : 2);
     c.spg = group_size == -1 || group_size == I ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
+    c.bt = T <= 4 ? 4 : MAXBT;
+    const int tiles = (N + MCOLS - 1) / MCOLS;
     int best = -1;   // places taken, in percent
-    const bool solo = T <= SOLO_T;
-    for (const int WK : {8, 4}) {
-        if (solo && WK == 4) continue;
-        const int tiles = (N + MCOLS * c.W / WK - 1) / (MCOLS * c.W / WK);
-        for (int cs = 1; cs <= 8; ++cs) {
-            const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
-            const int fit = std::max(1, few ? all / 2 : all);
-            const int waves = (tiles + fit - 1) / fit, use = (int)(100ll * tiles * cs / ((long long)waves * places));
-            if (use > best + 2) {
-                best = use;
-                c.WK = WK;
-                c.cluster = cs;
-            }
+    for (int cs = 1; cs <= 8; ++cs) {
+        const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
+        const int fit = std::max(1, few ? all / 2 : all);
+        const int waves = (tiles + fit - 1) / fit, use = (int)(100ll * tiles * cs / ((long long)waves * places));
+        if (use > best + 2) {
+            best = use;
+            c.cluster = cs;
         }
     }
-    if (solo) {
-        c.WK = 1;
-        c.bt = T <= 4 ? 4 : MAXBT;
+    c.rows = T > SUMS_T;
+    cut_smem(c, false, T, S, 0);
+    if (c.smem > max_smem(8)) {   // (groups of 32 or 64; never with rows, nor with up to 4 tokens)
+        c.rows = true;
         cut_smem(c, false, T, S, 0);
-        if (c.smem <= max_smem(8)) return c;
-        c.WK = 8;
-    }
-    // (many tokens and small groups: narrow tiles, then blocks of fewer slots; 2 always fit)
-    for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; c.bt /= 2) {
-        cut_smem(c, false, T, S, 0);
-        if (c.smem > max_smem(8)) {
-            c.WK = 8;
-            cut_smem(c, false, T, S, 0);
-        }
-        if (c.smem <= max_smem(8)) break;
     }
     return c;
 }
 
-template <int BITS, bool BF, int NT, bool UP, int W, int WK>
+template <int BITS, bool BF, int NT, bool UP, int W>
 wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, bool pdl, cudaStream_t stream) {
-    auto kern = moe_kernel<BITS, BF, NT, UP, W, WK>;
+    auto kern = moe_kernel<BITS, BF, NT, UP, W>;
     static std::atomic<uint64_t> attr_ctx[MAX_DEVICES];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
@@ -1139,29 +1206,22 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
         !make_map_rows(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, z, 2, dims, cols, planes, srows, sc, bp, p.sz_rows,
                        CU_TENSOR_MAP_SWIZZLE_NONE))
         return WQ_ERR_CUDA;
-    const int warp_tiles = UP ? (p.I + 31) / 32 : (p.NW + MCOLS - 1) / MCOLS;   // of 64 columns
-    auto go = [&](auto nt, auto w, auto wk) {
-        constexpr int NT = decltype(nt)::value, W = decltype(w)::value, WK = decltype(wk)::value;
-        constexpr int across = WK == 1 ? 1 : W / WK;   // warps along the columns
-        p.ntiles = (warp_tiles + across - 1) / across;
-        return launch_one<BITS, BF, NT, UP, W, WK>(tm, p, c.smem, pdl, stream);
-    };
-    using N1 = std::integral_constant<int, 1>;
-    using N2 = std::integral_constant<int, 2>;
-    using N4 = std::integral_constant<int, 4>;
-    using N8 = std::integral_constant<int, 8>;
-    using N16 = std::integral_constant<int, 16>;
+    const int tc = UP ? MCOLS / 2 * (c.W / 4) : MCOLS;   // columns of h or y per tile
+    p.ntiles = ((UP ? p.I : p.NW) + tc - 1) / tc;
     if constexpr (UP) {
-        if (c.W == 8) return go(N1{}, N8{}, N4{});
-        return c.bt <= 4 ? go(N1{}, N16{}, N4{}) : go(N2{}, N16{}, N4{});
+        if (c.W == 8) return launch_one<BITS, BF, 1, UP, 8>(tm, p, c.smem, pdl, stream);
+        return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, 16>(tm, p, c.smem, pdl, stream)
+                         : launch_one<BITS, BF, 2, UP, 16>(tm, p, c.smem, pdl, stream);
     } else {
-        if (c.bt <= 4) {
-            if (c.WK == 1) return go(N1{}, N8{}, N1{});
-            return c.WK == 4 ? go(N1{}, N8{}, N4{}) : go(N1{}, N8{}, N8{});
-        }
-        if (c.WK == 1) return go(N2{}, N8{}, N1{});
-        return c.WK == 4 ? go(N2{}, N8{}, N4{}) : go(N2{}, N8{}, N8{});
+        return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, down_warps(1)>(tm, p, c.smem, pdl, stream)
+                         : launch_one<BITS, BF, 2, UP, down_warps(2)>(tm, p, c.smem, pdl, stream);
     }
+}
+
+// Workspace: h's two bytes per value, then its steps (at most one per step of K); then DOWN's rows.
+size_t h_bytes(int S, int I) {
+    const size_t rows = (size_t)S * ((I + SK - 1) / SK);
+    return (rows * (2 * SK + 4) + 255) & ~(size_t)255;
 }
 
 template <int BITS, bool BF>
@@ -1184,7 +1244,7 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
     }
     const Cut up = last.up, down = last.down;
     p.Qh = (m.I + SK - 1) / SK;
-    p.hb = MCOLS * (up.W / up.WK) / 2 / SK;   // a tile of UP: 128 values or 64
+    p.hb = MCOLS * (up.W / 4) / 2 / SK;   // a tile of UP: 128 values or 64
     // (before anything is launched: what must fit 31 bits -- the weighted line of work, word rows, CTAs)
     const long long units = std::max((m.I + 31) / 32, (p.Qh + XBLK - 1) / XBLK), most = 1ll << 31;
     if (up.bt == 0 || down.bt == 0 || p.S * 4 * units >= most || (long long)p.E * (m.K * BITS / 32) >= most ||
@@ -1192,6 +1252,7 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
         return WQ_ERR_UNSUPPORTED;
     p.hq = static_cast<int8_t*>(m.ws);
     p.hstep = reinterpret_cast<float*>(p.hq + (size_t)2 * p.S * p.Qh * SK);
+    if (down.rows) p.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(m.ws) + h_bytes(p.S, m.I));
     p.NW = 2 * m.I;
     const wq_status st = run_product<BITS, BF, true>(p, m.w_up, m.s_up, m.z_up, m.K, m.group_size, up,
                                                      (m.flags & WQ_FLAG_PDL) != 0, stream);
@@ -1202,10 +1263,9 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
 
 }  // namespace
 
-// Workspace: h's two bytes per value, then its steps (at most one per step of K).
-size_t moe_workspace_bytes(int T, int top_k, int I) {
-    const size_t rows = (size_t)T * top_k * ((I + SK - 1) / SK);
-    return (rows * (2 * SK + 4) + 255) & ~(size_t)255;
+size_t moe_workspace_bytes(int T, int top_k, int I, int N) {
+    const size_t tiles = (N + MCOLS - 1) / MCOLS, rows = (size_t)T * top_k + MAXBT * 64;   // 64 warps in the largest cluster
+    return h_bytes(T * top_k, I) + (T > 4 ? tiles * rows * MCOLS * 4 : 0);
 }
 
 wq_status launch_moe(const MoeProblem& m, cudaStream_t stream) {
