@@ -188,7 +188,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // number, up to bt slots each, in the order of the slots.
 struct Head {
     int n;              // blocks
-    int i0, i1;         // this CTA's share
 };
 struct Blocks {         // in shared memory
     Head* h;
@@ -207,36 +206,25 @@ __host__ __device__ constexpr int table_bytes(int S) { return ((table_slots(S) +
 __device__ __forceinline__ int block_weight(int m) { return m <= 4 ? 3 : 4; }
 
 // Work is dealt out along a line: block u takes `units` of it (UP: its column tiles, DOWN: its fixed-point
-// blocks of K), each as heavy as the block's weight.  The first unit at or after part i of n, by a whole warp.
+// blocks of K), each as heavy as the block's weight.  The first unit at or after part i of n.
 __device__ __forceinline__ int share(const Blocks& b, int units, int i, int n) {
-    const int lane = threadIdx.x & 31;
-    const int C = b.start[b.h->n] * units;                       // below 2^31 (checked by the host)
-    const int c = C / n * i + C % n * i / n;                  // floor(C i / n) in 32 bits
-    const int q = c / units;
-    int u = -1;
-    for (int v0 = 0; v0 < b.h->n; v0 += 32)
-        u += __popc(__ballot_sync(0xffffffffu, v0 + lane < b.h->n && b.start[v0 + lane] <= q));
-    const int w = b.start[u + 1] - b.start[u];
-    return u * units + (c - b.start[u] * units + w - 1) / w;
+    const int nb = b.h->n;
+    if (nb == 0) return 0;
+    const int C = b.start[nb] * units;                           // below 2^31 (checked by the host)
+    const int c = C / n * i + C % n * i / n, q = c / units;      // c = floor(C i / n) in 32 bits
+    int lo = 0, hi = nb;                                         // start[lo] <= q < start[hi], but for q = start[nb]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (b.start[mid] <= q) lo = mid;
+        else hi = mid;
+    }
+    const int w = b.start[lo + 1] - b.start[lo];
+    return lo * units + (c - b.start[lo] * units + w - 1) / w;
 }
 
-// This CTA's share, by one warp, from the complete table: part `i` of `n`.
-__device__ __forceinline__ void share_out(const Blocks& b, int units, int i, int n) {
-    int i0 = 0, i1 = 0;
-    if (b.h->n > 0) {
-        i0 = share(b, units, i, n);
-        i1 = share(b, units, i + 1, n);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        b.h->i0 = i0;
-        b.h->i1 = i1;
-    }
-}
-
-// Fills the table and this CTA's share; every thread returns after both are complete.  cnt: scratch, E ints and S shorts.
+// Fills the table; every thread returns after it is complete.  cnt: scratch, E ints and S shorts.
 template <int MT>
-__device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b, int* cnt, int units, int part,
-                                            int parts) {
+__device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b, int* cnt) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned lt = (1u << lane) - 1u;
     if (p.S <= 32) {   // one slot per lane of one warp
@@ -274,8 +262,6 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
             }
             const int at = __shfl_sync(0xffffffffu, place, __ffs(same) - 1) + __popc(same & lt);
             if (id >= 0) b.order[at] = (int16_t)lane;
-            __syncwarp();
-            share_out(b, units, part, parts);
         }
         __syncthreads();
         return;
@@ -347,7 +333,6 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
             }
             __syncwarp();
         }
-        share_out(b, units, part, parts);
     }
     fence_proxy_async_smem();   // cnt lies where the copies will land
     __syncthreads();
@@ -441,16 +426,11 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const int ts = table_slots(p.S);
     int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
     const Blocks blk{&head, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
-    if constexpr (UP) find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), p.ntiles, blockIdx.x, gridDim.x);
-    else find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem), Q4, rank, p.cluster);
-    int at0 = head.i0, end = head.i1;
-    if constexpr (!UP) {   // this warp's
-        at0 = end = 0;
-        if (head.n > 0) {
-            at0 = share(blk, Q4, rank * MW + warp, p.cluster * MW);
-            end = share(blk, Q4, rank * MW + warp + 1, p.cluster * MW);
-        }
-    }
+    find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem));
+    // this CTA's part of the line (UP) or this warp's (DOWN): lane 0 finds where it starts, the others where it ends
+    const int part = UP ? (int)blockIdx.x : rank * MW + warp, parts = UP ? (int)gridDim.x : p.cluster * MW;
+    const int mine = share(blk, UP ? p.ntiles : Q4, part + (lane != 0), parts);
+    const int at0 = __shfl_sync(0xffffffffu, mine, 0), end = __shfl_sync(0xffffffffu, mine, 1);
     // ---- the items.  UP, the CTA's: (block, tile) pairs, all steps of K; DOWN, the warp's: one tile, runs of a block's steps.
     struct Item {
         int at, u, tile, s0, ns;   // position on the line, block, column tile; this warp's first step and steps
@@ -957,10 +937,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             float* const part = reinterpret_cast<float*>(smem + 8192);               // [slots of a few tokens][TC]
             constexpr int PART_ROWS = 192;
             for (int i = threadIdx.x; i < p.S; i += MT) place[i] = -1;
-            for (int w = warp; w <= nw; w += MW) {
-                const int v = head.n > 0 ? share(blk, Q4, w, nw) : 0;
-                if (lane == 0) starts[w] = v;
-            }
+            for (int w = threadIdx.x; w <= nw; w += MT) starts[w] = share(blk, Q4, w, nw);
             __syncthreads();
             for (int u = threadIdx.x; u < head.n; u += MT) {
                 int w0 = 0, w1 = nw;
