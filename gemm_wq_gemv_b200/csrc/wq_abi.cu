@@ -375,9 +375,8 @@ wq_status wq_device_status(int reset) {
     const wq_status c = wq::gemv_lean_device_status(reset);
     const wq_status d = wq::gptq_device_status(reset);
     const wq_status m = wq::moe_device_status(reset);
-    const wq_status l = wq::logprobs_device_status(reset);
     for (const wq_status e : {WQ_ERR_CUDA, WQ_ERR_TIMEOUT, WQ_ERR_CHECK})
-        if (a == e || b == e || c == e || m == e || l == e || (e == WQ_ERR_CUDA && d == e)) return e;
+        if (a == e || b == e || c == e || m == e || (e == WQ_ERR_CUDA && d == e)) return e;
     return d;
 }
 

@@ -103,7 +103,6 @@ wq_status launch_moe_route(const void* logits, int type, int T, int E, long long
 wq_status launch_logprobs(const void* logits, int type, int R, int V, long long ld, const int64_t* tokens, int top_k,
                           float* logprob, float* entropy, float* top_logprob, int64_t* top_id, unsigned flags,
                           cudaStream_t s);
-wq_status logprobs_device_status(int reset);
 
 // 2-D tiled TMA descriptor for a row-major (outer, inner) array.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,

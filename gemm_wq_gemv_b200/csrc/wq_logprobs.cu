@@ -29,10 +29,6 @@
 #include "wq_ptx.cuh"
 
 namespace wq {
-
-// Device status of this kernel: bit 1 once a check of the checked build failed.
-__device__ unsigned int g_logprobs_status = 0;
-
 namespace {
 
 constexpr int LT = 256;        // threads per CTA
@@ -458,16 +454,6 @@ wq_status launch_logprobs(const void* logits, int type, int R, int V, long long 
     if (type == WQ_TYPE_F32) return run_lp<WQ_TYPE_F32>(p, R, pdl, s);
     if (type == WQ_TYPE_F16) return run_lp<WQ_TYPE_F16>(p, R, pdl, s);
     return run_lp<WQ_TYPE_BF16>(p, R, pdl, s);
-}
-
-wq_status logprobs_device_status(int reset) {
-    unsigned int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_logprobs_status, sizeof(v)) != cudaSuccess) return WQ_ERR_CUDA;
-    if (reset) {
-        const unsigned int zero = 0;
-        if (cudaMemcpyToSymbol(g_logprobs_status, &zero, sizeof(zero)) != cudaSuccess) return WQ_ERR_CUDA;
-    }
-    return (v & 2u) ? WQ_ERR_CHECK : WQ_OK;
 }
 
 }  // namespace wq

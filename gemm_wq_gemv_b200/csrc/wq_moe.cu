@@ -12,7 +12,7 @@
 // be bound by HBM.
 //  * Work split.  Slots are grouped by expert into blocks of bt slots (up to 8;
 //    fewer when K is very long), so an expert's words are read once for them.  Every
-//    CTA derives the blocks from the ids.  UP (one CTA of 16 warps per SM): the
+//    CTA derives the blocks from the ids.  UP (one CTA per SM): the
 //    (block, column tile) pairs, all of K each, are dealt out over the SMs in runs of
 //    equal weight; its warps split K and the tile's columns, 64 columns each (32 gate and
 //    the matching 32 up columns, so the activation needs no second pass), and their
@@ -47,7 +47,7 @@
 //    point of any value costs nothing per code.  At the end of a block (or group):
 //    acc += s * step * (D - z X) in fp32, D = 256 D_hi + D_lo.
 //  * Loads.  A warp's words come by TMA, 16 word rows x 64 columns per stage (4 KB)
-//    with the s and z rows of its groups, into a private ring of two stages: 64 to
+//    with the s and z rows of its groups, into a private ring of two stages: 96 to
 //    128 KB in flight per SM.  The 128-byte swizzle and the column order of the lanes
 //    (chunk cg) keep the 16-byte reads free of bank conflicts.  (cp.async by every
 //    lane, which this replaced, cost 19 instructions per step of 32 values, a quarter
@@ -86,10 +86,13 @@ constexpr int XBLK = 4;         // steps per block of fixed-point values
 constexpr int BOX_ROWS = 16;    // word rows per TMA box
 constexpr int STAGE = 2 * BOX_ROWS * 128;   // bytes: two halves
 constexpr int NST = 2;          // ring stages per warp (DOWN with 3: the same time)
-// Warps of a CTA of DOWN.  Two token tiles need 160 registers: with 8 warps of 128 the spilled ones passed through
-// L2, shared memory leaving little L1 (16 tokens, 2 of 8 experts: 139 us against 122 us; 48 tokens, 8-bit: 111 us
-// against 96 us).  With one token tile, 8 (1 token: 15.5 us against 18.9 us).
+// Warps of a CTA with NT token tiles.  Two tiles need about 160 registers: with 16 warps per SM, and 128, the spilled
+// ones passed through L2, shared memory leaving little L1.  So 12 per SM, UP 12 in one CTA, DOWN 6 in each of two
+// (DOWN, 16 tokens, 2 of 8 experts: 139 us against 122 us; 48 tokens, 8-bit: 111 us against 96 us; UP, 48 tokens:
+// 90 us against 88 us).  One tile: 16 per SM (1 token, DOWN: 14.6 us; with 6 in a CTA 18 us).
+constexpr int up_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int down_warps(int nt) { return nt == 1 ? 8 : 6; }
+constexpr int along_k(int warps) { return warps == 12 ? 3 : 4; }   // warps of a CTA of UP along K
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 template <int BITS> constexpr int step_rows() { return SK * BITS / 32; }   // word rows per step: 4 or 8
@@ -186,11 +189,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 // The blocks of a launch: experts in the order of their first slot (S <= 32) or of their
 // number, up to bt slots each, in the order of the slots.
-struct Head {
-    int n;              // blocks
-};
 struct Blocks {         // in shared memory
-    Head* h;
+    int* n;             // blocks
     int* start;         // sum of the weights of the blocks before u, and of all
     int16_t* e;         // expert of block u
     int16_t* first;     // its first slot's place in `order`
@@ -201,14 +201,14 @@ struct Blocks {         // in shared memory
 __host__ __device__ constexpr int table_slots(int S) { return S < 32 ? 32 : S; }
 __host__ __device__ constexpr int table_bytes(int S) { return ((table_slots(S) + 1) * 4 + (3 * table_slots(S) + 1) * 2 + 15) / 16 * 16; }
 
-// Weight of a block of m slots: an item with two token tiles took 1.36 times as long (14.5 us against
-// 10.7 us for 4096 x 256 4-bit columns).
-__device__ __forceinline__ int block_weight(int m) { return m <= 4 ? 3 : 4; }
+// Weight of a block of m slots: two token tiles take more instructions, the same loads.  (16 tokens, 2 of 8 experts,
+// 4-bit | 48 tokens, 8-bit: with 4 : 5 120.5 | 83.8 us, 3 : 4 121.3 | 88.3, 2 : 3 129 | 89, 1 : 1 132 | 84.)
+__device__ __forceinline__ int block_weight(int m) { return m <= 4 ? 4 : 5; }
 
 // Work is dealt out along a line: block u takes `units` of it (UP: its column tiles, DOWN: its fixed-point
 // blocks of K), each as heavy as the block's weight.  The first unit at or after part i of n.
 __device__ __forceinline__ int share(const Blocks& b, int units, int i, int n) {
-    const int nb = b.h->n;
+    const int nb = *b.n;
     if (nb == 0) return 0;
     const int C = b.start[nb] * units;                           // below 2^31 (checked by the host)
     const int c = C / n * i + C % n * i / n, q = c / units;      // c = floor(C i / n) in 32 bits
@@ -248,7 +248,7 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
                 }
             }
             if (lane == 31) {
-                b.h->n = pre;
+                *b.n = pre;
                 b.start[pre] = cost;
                 b.first[pre] = (int16_t)place;
             }
@@ -300,7 +300,7 @@ __device__ __forceinline__ void find_blocks(const MoeParams& p, const Blocks& b,
             }
         }
         if (lane == 31) {
-            b.h->n = pre;
+            *b.n = pre;
             b.start[pre] = cost;
             b.first[pre] = (int16_t)place;
         }
@@ -391,13 +391,13 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     constexpr int RPS = step_rows<BITS>();       // 4 or 8
     constexpr int RL = RPS / 4;                  // word rows per lane and step
     constexpr int SPS = BOX_ROWS / RPS;          // steps per stage
-    constexpr int WK = UP ? 4 : 1;               // UP: warps along K
+    constexpr int WK = UP ? along_k(MW) : 1;               // UP: warps along K
     constexpr int WC = UP ? MW / WK : 1;         // and along the columns.  DOWN: every warp works alone
     constexpr int TC = MCOLS * WC;               // weight columns per tile
     extern __shared__ uint8_t smem_raw[];
     // the 128-byte swizzle of the TMA boxes repeats every 1024 bytes
     uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-    __shared__ Head head;
+    __shared__ int nblocks;
     __shared__ uint64_t bars[MW * NST], free_bar;   // free_bar (UP): the partials have been read
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -425,7 +425,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     uint8_t* const tab = smem + roff + table_at(RW, p.bt);
     const int ts = table_slots(p.S);
     int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
-    const Blocks blk{&head, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
+    const Blocks blk{&nblocks, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
     find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem));
     // this CTA's part of the line (UP) or this warp's (DOWN): lane 0 finds where it starts, the others where it ends
     const int part = UP ? (int)blockIdx.x : rank * MW + warp, parts = UP ? (int)gridDim.x : p.cluster * MW;
@@ -797,6 +797,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             }
             if constexpr (!UP) {
                 if (p.rows != nullptr) {   // the rows of this (warp, block), to be summed at the end
+                    if (!check(blk.first[it.u] + bm + p.bt * (rank * MW + warp) <= p.S + p.bt * MW * p.cluster,
+                               &g_moe_status))
+                        return;
                     float* const to = p.rows + ((size_t)it.tile * (p.S + p.bt * MW * p.cluster) + blk.first[it.u] +
                                                 p.bt * (rank * MW + warp)) * TC + 4 * cg;
 #pragma unroll
@@ -939,7 +942,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             for (int i = threadIdx.x; i < p.S; i += MT) place[i] = -1;
             for (int w = threadIdx.x; w <= nw; w += MT) starts[w] = share(blk, Q4, w, nw);
             __syncthreads();
-            for (int u = threadIdx.x; u < head.n; u += MT) {
+            for (int u = threadIdx.x; u < nblocks; u += MT) {
                 int w0 = 0, w1 = nw;
                 while (w0 < nw - 1 && starts[w0 + 1] <= u * Q4) ++w0;
                 while (w1 > w0 + 1 && starts[w1 - 1] >= (u + 1) * Q4) --w1;
@@ -957,7 +960,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                     const int r = i / (TC / 4), c = 4 * (i % (TC / 4));
                     const int sl = (rank + (k0 + r / p.top_k) * p.cluster) * p.top_k + r % p.top_k;
                     float4 v = zero;
-                    if (place[sl] >= 0 && check(sl < p.S, &g_moe_status)) {
+                    if (check(sl < p.S, &g_moe_status) && place[sl] >= 0 &&
+                        check(place[sl] + p.bt * (wlast[sl] - 1) < ns && wlast[sl] <= nw, &g_moe_status)) {
                         const float a = p.weights[sl];
                         const float* const from = p.rows + ((size_t)tl * ns + place[sl]) * TC + c;
                         for (int w = wfirst[sl]; w < wlast[sl]; w += 2) {   // (a run may be empty)
@@ -1008,8 +1012,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     }
 }
 
-// Dynamic shared memory a CTA of 16 warps (one per SM) or 8 (two) can have.
-constexpr int max_smem(int W) { return W == 16 ? 225 * 1024 : 112 * 1024; }
+// Dynamic shared memory a CTA of 12 or 16 warps (one per SM), or of 6 or 8 (two), can have.
+constexpr int max_smem(int W) { return W > 8 ? 225 * 1024 : 112 * 1024; }
 constexpr int ring_bytes(int W, int sz_rows) { return 1024 + W * NST * (STAGE + 256 * sz_rows); }
 // s rows of the groups that a stage of `sps` steps, starting at a multiple of them, can touch.
 int stage_groups(int spg, int sps) { return spg % sps == 0 ? 1 : std::min(sps, (sps - 1) / spg + 2); }
@@ -1037,11 +1041,12 @@ void cut_smem(Cut& c, bool up, int T, int S, int Q) {
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
 // leave room for (bt = 0: K is too long).
 //  * Few tokens, and no more tiles of 64 values of h than SMs: CTAs of 8 warps, beside which DOWN's start while
-//    they run (1 token, 8 experts of 2048 x 1024: 16.2 us against 19.7 us with 16 warps; with 344 tiles, 2 experts of
+//    they run (1 token, 8 experts of 2048 x 1024: 16.2 us against 19.7 us with 16; with 344 tiles, 2 experts of
 //    4096 x 11008, 59 us against 45 us).
-//  * Else 16 warps and tiles of 128 values, 4 warps along K.  (8 along K and tiles of 64, where that fills the SMs'
-//    last round better, measured slower: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64 experts of 2048 x
-//    1024: 96 us against 81 us.)
+//  * Else one CTA per SM and tiles of 128 values, 3 or 4 warps along K.  (Tiles of 64, where that fills the SMs' last
+//    round better, measured slower: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64 experts of 2048 x
+//    1024: 96 us against 81 us.  So did pairs of CTAs that halve the odd item of their part of the line: 48 tokens,
+//    8-bit, 99 us against 88 us; 1 token, 2 experts of 4096 x 11008, 40 us against 42 us.)
 Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
     const int Q = (K + SK - 1) / SK;
     Cut c{};
@@ -1054,15 +1059,15 @@ Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
         cut_smem(c, true, T, S, Q);
         if (c.smem <= max_smem(8)) return c;
     }
-    c.W = 16;
+    c.W = up_warps(T <= 4 ? 1 : 2);
     for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; --c.bt) {
         cut_smem(c, true, T, S, Q);
-        if (c.smem <= max_smem(16)) break;
+        if (c.smem <= max_smem(c.W)) break;
     }
     return c;
 }
 
-// Clusters of cs CTAs of 8 warps, two per SM, that the device holds at once (a GPC's SMs are not a multiple of
+// Clusters of cs CTAs of DOWN, two per SM, that the device holds at once (a GPC's SMs are not a multiple of
 // every size: 15 clusters of 8 with one CTA per SM on a B200, not 148 / 8 = 18).  Asked once per device.
 int clusters_that_fit(int cs) {
     static std::atomic<int> known[MAX_DEVICES][9];
@@ -1094,10 +1099,9 @@ int clusters_that_fit(int cs) {
     return n;
 }
 
-// DOWN: CTAs of 8 warps.  A column tile is worked on by a cluster, of the size (and with the width of tile) that
-// leaves the fewest places of the SMs without a CTA: two per SM, so that one streams while the other ends an item,
-// or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit an empty
-// device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
+// DOWN: a column tile is worked on by a cluster, of the size that leaves the fewest places of the SMs without a CTA:
+// two per SM, or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit
+// an empty device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
 Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
     const int places = few ? sm_count() : 2 * sm_count();
     Cut c{};
@@ -1183,12 +1187,12 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
         !make_map_rows(&tm[2], CU_TENSOR_MAP_DATA_TYPE_UINT16, z, 2, dims, cols, planes, srows, sc, bp, p.sz_rows,
                        CU_TENSOR_MAP_SWIZZLE_NONE))
         return WQ_ERR_CUDA;
-    const int tc = UP ? MCOLS / 2 * (c.W / 4) : MCOLS;   // columns of h or y per tile
+    const int tc = UP ? MCOLS / 2 * (c.W / along_k(c.W)) : MCOLS;   // columns of h or y per tile
     p.ntiles = ((UP ? p.I : p.NW) + tc - 1) / tc;
     if constexpr (UP) {
         if (c.W == 8) return launch_one<BITS, BF, 1, UP, 8>(tm, p, c.smem, pdl, stream);
-        return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, 16>(tm, p, c.smem, pdl, stream)
-                         : launch_one<BITS, BF, 2, UP, 16>(tm, p, c.smem, pdl, stream);
+        return c.W == up_warps(1) ? launch_one<BITS, BF, 1, UP, up_warps(1)>(tm, p, c.smem, pdl, stream)
+                         : launch_one<BITS, BF, 2, UP, up_warps(2)>(tm, p, c.smem, pdl, stream);
     } else {
         return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, down_warps(1)>(tm, p, c.smem, pdl, stream)
                          : launch_one<BITS, BF, 2, UP, down_warps(2)>(tm, p, c.smem, pdl, stream);
@@ -1221,10 +1225,10 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
     }
     const Cut up = last.up, down = last.down;
     p.Qh = (m.I + SK - 1) / SK;
-    p.hb = MCOLS * (up.W / 4) / 2 / SK;   // a tile of UP: 128 values or 64
+    p.hb = MCOLS * (up.W / along_k(up.W)) / 2 / SK;   // a tile of UP: 128 values or 64
     // (before anything is launched: what must fit 31 bits -- the weighted line of work, word rows, CTAs)
     const long long units = std::max((m.I + 31) / 32, (p.Qh + XBLK - 1) / XBLK), most = 1ll << 31;
-    if (up.bt == 0 || down.bt == 0 || p.S * 4 * units >= most || (long long)p.E * (m.K * BITS / 32) >= most ||
+    if (up.bt == 0 || down.bt == 0 || p.S * 5 * units >= most || (long long)p.E * (m.K * BITS / 32) >= most ||
         (long long)p.E * ((long long)m.I * BITS / 32) >= most || (m.N + 63ll) / 64 * 8 >= most)
         return WQ_ERR_UNSUPPORTED;
     p.hq = static_cast<int8_t*>(m.ws);

@@ -430,7 +430,6 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  */
 #define WQ_MOE_MAX_TOKENS 64
 #define WQ_MOE_MAX_K 24576
-#define WQ_MOE_MAX_SLOTS (WQ_MOE_MAX_TOKENS * 16)
 #define WQ_ACT_SILU 0
 #define WQ_ACT_GELU 1
 size_t wq_moe_workspace_size(int T, int top_k, int inner, int N);
@@ -455,8 +454,9 @@ wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, co
  *   top_logprob, top_id  given if top_k > 0, else NULL.
  * One pass over the logits in fp32.  Masked entries may be -inf or the type's
  * lowest value.  A row that holds NaN or +inf, or nothing but -inf, has NaN
- * logprob (of a token inside the vocabulary), entropy and top_logprob.  1 <= R <= 2^24, 1 <= V < 2^30, 0 <= top_k <=
- * min(V, 32).  flags: 0 or WQ_FLAG_PDL, as wq_moe_route.
+ * logprob (of a token inside the vocabulary), entropy and top_logprob.
+ * 1 <= R <= 2^24, 1 <= V < 2^30, 0 <= top_k <= min(V, 32).  flags: 0 or
+ * WQ_FLAG_PDL, as wq_moe_route.
  */
 wq_status wq_logprobs(const void* logits, int type, int R, int V, int64_t ld, const int64_t* tokens, int top_k,
                       float* logprob, float* entropy, float* top_logprob, int64_t* top_id, unsigned flags,
@@ -477,7 +477,8 @@ wq_status wq_device_status(int reset);
  * the products (wq_gemv, wq_gemm and their plans) checks the index of each
  * global and shared-memory access it computes itself
  * (x, y, the split-K workspace, the s/z rows and the staging buffers; the TMA
- * copies are bounded by their descriptors) against the array it belongs to;
+ * copies are bounded by their descriptors) against the array it belongs to, and
+ * wq_moe its slots, its staged values and the rows it sums;
  * an access that fails is skipped and recorded, and wq_device_status then
  * returns WQ_ERR_CHECK (after WQ_ERR_TIMEOUT, which it reports first).  It is
  * the stand-in for a memory checker: slower, for tests.
