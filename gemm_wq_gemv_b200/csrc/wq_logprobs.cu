@@ -20,6 +20,13 @@
 //    read again, from L2, and the few entries at or above the floor are
 //    ranked by counting.  Keys (value, index) are unique, so the result does not
 //    depend on the order in which entries are collected.
+// Measured (B200, device time): 2048 rows of 128000 bf16, 1 alternative, 524 MB: 92 us,
+// 5.7 TB/s, 87 % of the copy rate; what is left is the rows' ends (the joins and the
+// re-read, about 1 us per row, overlap with other CTAs' streams only).  Five CTAs of 256
+// threads per SM: 4 take 98.6 us (94 with 8 vectors in flight per thread instead of 4), 6
+// take 103 (registers), CTAs of 128 threads 100.  64 rows of 50001 bf16, 20 alternatives,
+// 6.4 MB: 13.7 us; 32 rows of 128000 fp32, 16 MB: 9.3 us; one row of 32000 fp16: 6.4 us --
+// chains of loads, joins and ranking, not bytes.
 #include <cuda_runtime.h>
 
 #include <algorithm>

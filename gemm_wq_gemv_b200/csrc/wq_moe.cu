@@ -23,10 +23,9 @@
 //    copies are joined at the end, across the cluster through distributed shared memory.
 //    With more, the copies do not fit: a warp leaves the rows of its (block, part) in
 //    global memory (L2), and the cluster sums them at its end.  Both in a fixed order.
-//    (Measured: rows instead of copies, 16 tokens of 64 experts: 71 us against 64 us;
-//    instead of a split of K over the CTA's warps with two barriers per item, 32 tokens:
-//    85 us against 95 us; one copy per CTA with the warps adding in turn: 97 us; a last
-//    CTA to arrive that sums rows: 1 us per item for the fence and up to 17 us at the end.)
+//    (Instead of rows, 32 tokens: 85 us; a split of K over the CTA's warps with two
+//    barriers per item 95 us, one copy per CTA with the warps adding in turn 97 us; a last
+//    CTA to arrive that sums rows cost 1 us per item for the fence, up to 17 us at the end.)
 //  * Products on integers.  Unpacking codes to fp16 or bf16 costs 7 instructions
 //    per word of 8 codes, and with m16n8k16 (2.1 clocks per SM on B200) that held
 //    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
@@ -54,10 +53,13 @@
 //    of all.)
 //  * DOWN is a programmatic dependent of UP: it finds its blocks and requests its
 //    first words while UP drains, and waits only before it reads h.
-// Measured (B200): 16 tokens, 2 of 8 experts of 4096 x 11008, 4-bit, 569 MB: 152 us,
-// 3.7 TB/s; UP reads at 4.8 TB/s and is held by its last round of items and, where an
-// expert has more than 4 tokens, by instruction issue (a second MMA per operand and
-// twice the folds); DOWN by instruction issue.
+// Measured (B200, device time): 16 tokens, 2 of 8 experts of 4096 x 11008, 4-bit, 569 MB:
+// 120 us, 4.7 TB/s (UP 66 us for 383 MB, DOWN 53 us for 195 MB); 48 tokens, 4 of 32 experts
+// of 2048 x 1408, 8-bit, 285 MB: 83 us, 3.4 TB/s; 1 token, 8 of 64 experts of 2048 x 1024,
+// 4-bit, 27 MB: 14.6 us.  UP is held by its SMs' last items (12 to 20 us each; a part of the
+// line is 2 to 6 of them) and, where an expert has more than 4 tokens, by a second MMA per
+// operand and twice the folds; DOWN by the latency of its chain, a stage every 2000 cycles
+// per warp; 1 token by the two starts (blocks, first loads, the join: 9 of 14.6 us).
 // Every mbarrier wait is bounded; on time-out the kernel records it in its status
 // word and skips the rest of the warp's work.
 #include <cuda_bf16.h>
@@ -80,7 +82,10 @@ namespace {
 
 constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
 constexpr int MAXBT = 8;        // slots per block
-constexpr int SUMS_T = 16;      // most tokens for which every warp of DOWN keeps sums of y of its own
+// Most tokens for which every warp of DOWN keeps sums of y of its own; with more it leaves rows in global memory.  (Rows
+// against sums, 16 tokens of 64 experts: 59.7 us against 55.7; 5 tokens, small: 18.5 us against 13.7; 32 tokens, for
+// which sums would fit with groups of 64 or more only: 72.6 us against 70.0.)
+constexpr int SUMS_T = 16;
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
 constexpr int BOX_ROWS = 16;    // word rows per TMA box
@@ -1121,11 +1126,7 @@ Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
         }
     }
     c.rows = T > SUMS_T;
-    cut_smem(c, false, T, S, 0);
-    if (c.smem > max_smem(8)) {   // (groups of 32 or 64; never with rows, nor with up to 4 tokens)
-        c.rows = true;
-        cut_smem(c, false, T, S, 0);
-    }
+    cut_smem(c, false, T, S, 0);   // (at most 92 KB)
     return c;
 }
 
@@ -1246,7 +1247,7 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
 
 size_t moe_workspace_bytes(int T, int top_k, int I, int N) {
     const size_t tiles = (N + MCOLS - 1) / MCOLS, rows = (size_t)T * top_k + MAXBT * 64;   // 64 warps in the largest cluster
-    return h_bytes(T * top_k, I) + (T > 4 ? tiles * rows * MCOLS * 4 : 0);
+    return h_bytes(T * top_k, I) + (T > SUMS_T ? tiles * rows * MCOLS * 4 : 0);
 }
 
 wq_status launch_moe(const MoeProblem& m, cudaStream_t stream) {

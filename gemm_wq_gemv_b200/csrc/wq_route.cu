@@ -9,7 +9,10 @@
 // row is read once and nothing is shared.  top_k rounds: each lane offers its
 // best remaining entry, one redux finds the largest key and a second the lowest
 // index that holds it.  The row is a few hundred bytes: a call is bound by
-// launch latency for a few tokens, and by the rounds (two reductions each) for many.
+// launch latency for a few tokens, and by the rounds (two reductions each, which
+// wait for each other) for many.  Measured (B200, device time): 1 row of 64 fp32
+// logits, 8 chosen, 2.2 us; 8192 rows of 128 bf16, 8 chosen, 6.7 us for 2.6 MB
+// (0.4 us at copy rate); 1000 rows of 500 fp16, 10 chosen, 5.5 us.
 #include <cuda_runtime.h>
 
 #include "wq_internal.h"

@@ -1,10 +1,15 @@
 """The mixture-of-experts layer against the 64-bit definition (moe_oracle.py has the bound)."""
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 
 import moe_oracle
 from guard import Guarded
 
 pytestmark = pytest.mark.gpu
+ROOT = Path(__file__).resolve().parents[1]
 
 # T, E, k, K, I, N, bits, G, dtype, act, frac
 CASES = [
@@ -37,6 +42,9 @@ CASES = [
     (2, 2, 1, 20000, 16, 8, 8, -1, "fp16", "silu", False),       # one slot per block
     (6, 2, 1, 64, 6176, 24, 4, 32, "fp16", "silu", True),        # a long inner length: K splits
     (1, 2, 2, 32, 8776, 16, 8, -1, "bf16", "gelu", False),
+    (20, 2, 1, 64, 6176, 24, 4, 32, "bf16", "silu", False),      # a block's rows from many warps
+    (18, 3, 2, 64, 352, 72, 8, -1, "fp16", "silu", True),
+    (40, 16, 16, 32, 32, 19208, 8, 32, "fp16", "silu", False),   # no cluster: the rows are summed a few tokens at a time
 ]
 
 
@@ -223,6 +231,34 @@ def test_streams_and_graphs(cuda, libwq):
         moe_oracle.assert_close(ys[i][0], *refs[i])
     moe_oracle.assert_close(outs[0], *refs[2])
     moe_oracle.assert_close(outs[1], *refs[1])
+
+
+@pytest.mark.parametrize("T", [1, 12, 24])
+def test_first_call_is_captured(cuda, T):
+    """A process whose first call of the layer is recorded in a graph; the replays give the eager bits."""
+    code = f"""
+import sys
+sys.path.insert(0, "tests")
+import torch, moe_oracle
+import gemm_wq_gemv_b200 as wq
+p = moe_oracle.problem({T}, 6, 2, 256, 128, 136, 4, 64, torch.bfloat16, seed=31)
+ref, tol = moe_oracle.layer(p, 4, "silu")
+dev = torch.device("cuda:0")
+a, w = moe_oracle.to_gpu(wq, p, 4, dev)
+plan = wq.MoePlan(*w, 4, 64, {T}, 2, pdl=True)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = plan(*a)
+for _ in range(3):
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    moe_oracle.assert_close(y, ref, tol)
+assert torch.equal(y, plan(*a)) and wq.device_status() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
 
 
 def test_refusals(cuda, libwq):
