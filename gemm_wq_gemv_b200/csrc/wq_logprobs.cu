@@ -25,7 +25,7 @@
 // re-read, about 1 us per row, overlap with other CTAs' streams only).  Five CTAs of 256
 // threads per SM: 4 take 98.6 us (94 with 8 vectors in flight per thread instead of 4), 6
 // take 103 (registers), CTAs of 128 threads 100.  64 rows of 50001 bf16, 20 alternatives,
-// 6.4 MB: 13.7 us; 32 rows of 128000 fp32, 16 MB: 9.3 us; one row of 32000 fp16: 6.4 us --
+// 6.4 MB: 11.5 us; 32 rows of 128000 fp32, 16 MB: 9.3 us; one row of 32000 fp16: 6.4 us --
 // chains of loads, joins and ranking, not bytes.
 #include <cuda_runtime.h>
 
@@ -438,11 +438,16 @@ wq_status launch_lp(const LpParams& p, int R, bool pdl, cudaStream_t s) {
 
 template <int TYPE>
 wq_status run_lp(const LpParams& p, int R, bool pdl, cudaStream_t s) {
-    // Split a row while the CTAs fill the SMs no more than four times and each
-    // keeps at least one vector per thread.
+    // A row is split while there is an SM for every CTA and each keeps a vector per thread, and on to four CTAs per SM
+    // where each keeps 12 (bf16, 128 rows: of 128000, 4 CTAs per row 14.7 us, 2 15.9, 1 20.4; of 32000, 1 6.5 us, 2 7.7,
+    // 4 8.4; 64 rows of 128000: 4 11.3 us, 8 12.8, 2 13.8).
     const int nv = p.V / Vec<TYPE>::N;
     int cs = 1;
-    while (cs < 8 && (long long)R * cs * 2 <= 4ll * sm_count() && nv >= cs * 2 * LT) cs *= 2;
+    while (cs < 8) {
+        const long long ctas = (long long)R * cs * 2;
+        if (ctas > 4ll * sm_count() || nv < cs * 2 * LT * (ctas > sm_count() ? 12 : 1)) break;
+        cs *= 2;
+    }
     switch (cs) {
         case 8: return launch_lp<TYPE, 8>(p, R, pdl, s);
         case 4: return launch_lp<TYPE, 4>(p, R, pdl, s);
