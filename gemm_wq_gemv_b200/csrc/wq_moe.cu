@@ -626,7 +626,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             // B column g of token tile n: UP from shared memory; DOWN straight from global memory, a stage ahead (every
             // CTA reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
             uint32_t xa[AT], sp[AT];               // UP
-            uint32_t hp[AT], hs[AT];               // DOWN: values and steps (below 2^31: checked by the host)
+            uint32_t hp[AT], hs[AT];               // DOWN: offsets of values and steps (wq_moe refuses 2^31 bytes)
             uint2 bx[SPS][AT];
             float step_next[2][AT];
             [[maybe_unused]] float wt[AT];         // DOWN: weights of the slots 4 n + t and their rows of y's sums

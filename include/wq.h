@@ -401,7 +401,8 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  * A mixture-of-experts layer on packed weights, for a few tokens:
  *   h[t][j] = act(x[t] @ Wg[e]) * (x[t] @ Wu[e]),  e = ids[t][j]
  *   y[t]    = sum_j weights[t][j] * (h[t][j] @ Wd[e])
- * in two launches; each chosen expert's words are read once.
+ * in two launches; a chosen expert's words are read once for every 8 slots that it
+ * has (fewer with a K above 5000).
  *   x        (T, K), y (T, N): binary16, or bfloat16 with WQ_FLAG_BF16, as all s and z.
  *   ids      (T, top_k) int32, weights (T, top_k) fp32: as wq_moe_route writes
  *            them.  An id outside 0 .. E-1 leaves its slot empty; a token whose
@@ -423,8 +424,10 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  * bits 4 or 8 (else WQ_ERR_UNSUPPORTED).  1 <= T <= WQ_MOE_MAX_TOKENS,
  * 1 <= top_k <= 16, 1 <= E <= WQ_MOE_MAX_EXPERTS, K <= WQ_MOE_MAX_K.  K and
  * inner multiples of eps and of the group size (-1: one group per column), the
- * group size a multiple of 32 (else WQ_ERR_UNSUPPORTED); inner and N multiples of 8.  Arrays of 16-bit
- * values and words 16-byte aligned, ids and weights 4-byte.  flags:
+ * group size a multiple of 32 (else WQ_ERR_UNSUPPORTED); inner and N multiples of
+ * 8; T * top_k * inner below 2^30, and E times the word rows of either array below
+ * 2^31 (else WQ_ERR_UNSUPPORTED).  Arrays of 16-bit values and words 16-byte
+ * aligned, ids and weights 4-byte.  flags:
  * WQ_FLAG_BF16, WQ_FLAG_PDL (all inputs are read after the previous kernel on
  * the stream has completed).
  */

@@ -45,6 +45,7 @@ def test_moe_argument_checks(libwq):
                         ctypes.c_size_t(need if nbytes is None else nbytes), None)
     assert call(bits=3) == UNS and call(bits=5) == UNS and call(act=2) == UNS and call(G=16) == UNS
     assert call(K=24576 + 64) == UNS and call(bits=8, G=16) == UNS
+    assert call(T=64, k=16, I=1 << 20, G=-1, nbytes=1 << 50) == UNS       # h of all slots passes 2^31 bytes
     for bad in (dict(T=0), dict(T=65, nbytes=1 << 40), dict(K=0), dict(K=252, G=-1), dict(I=0), dict(I=-8), dict(N=0),
                 dict(E=0), dict(E=513), dict(k=0), dict(k=17, nbytes=1 << 40), dict(G=0), dict(G=96), dict(flags=2),
                 dict(flags=8), dict(ws=None), dict(nbytes=need - 1), dict(I=1 << 30)):
