@@ -93,8 +93,9 @@ constexpr int STAGE = 2 * BOX_ROWS * 128;   // bytes: two halves
 constexpr int NST = 2;          // ring stages per warp (DOWN with 3: the same time)
 // Warps of a CTA with NT token tiles.  Two tiles need about 160 registers: with 16 warps per SM, and 128, the spilled
 // ones passed through L2, shared memory leaving little L1.  So 12 per SM, UP 12 in one CTA, DOWN 6 in each of two
-// (DOWN, 16 tokens, 2 of 8 experts: 139 us against 122 us; 48 tokens, 8-bit: 111 us against 96 us; UP, 48 tokens:
-// 90 us against 88 us).  One tile: 16 per SM (1 token, DOWN: 14.6 us; with 6 in a CTA 18 us).
+// (DOWN with 8: 16 tokens, 2 of 8 experts, 148 us against 121 us; 16 of 64 experts 62.5 against 55.6; 48 tokens, 8-bit,
+// 88.6 against 83.5; UP with 16: 48 tokens 90 against 88, 16 tokens 120 against 121).  One tile: 16 per SM (1 token:
+// 14.6 us; DOWN with 6 in a CTA 15.8).
 constexpr int up_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int down_warps(int nt) { return nt == 1 ? 8 : 6; }
 constexpr int along_k(int warps) { return warps == 12 ? 3 : 4; }   // warps of a CTA of UP along K
@@ -204,7 +205,9 @@ struct Blocks {         // in shared memory
     __device__ __forceinline__ int count(int u) const { return first[u + 1] - first[u]; }
 };
 __host__ __device__ constexpr int table_slots(int S) { return S < 32 ? 32 : S; }
-__host__ __device__ constexpr int table_bytes(int S) { return ((table_slots(S) + 1) * 4 + (3 * table_slots(S) + 1) * 2 + 15) / 16 * 16; }
+__host__ __device__ constexpr int table_bytes(int S) {
+    return ((table_slots(S) + 1) * 4 + (3 * table_slots(S) + 1) * 2 + 15) / 16 * 16;
+}
 
 // Weight of a block of m slots: two token tiles take more instructions, the same loads.  (16 tokens, 2 of 8 experts,
 // 4-bit | 48 tokens, 8-bit: with 4 : 5 120.5 | 83.8 us, 3 : 4 121.3 | 88.3, 2 : 3 129 | 89, 1 : 1 132 | 84.)
@@ -436,7 +439,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const int part = UP ? (int)blockIdx.x : rank * MW + warp, parts = UP ? (int)gridDim.x : p.cluster * MW;
     const int mine = share(blk, UP ? p.ntiles : Q4, part + (lane != 0), parts);
     const int at0 = __shfl_sync(0xffffffffu, mine, 0), end = __shfl_sync(0xffffffffu, mine, 1);
-    // ---- the items.  UP, the CTA's: (block, tile) pairs, all steps of K; DOWN, the warp's: one tile, runs of a block's steps.
+    // ---- the items.  UP, the CTA's: (block, tile) pairs, all steps of K; DOWN, the warp's: one tile, runs of a
+    // block's steps
     struct Item {
         int at, u, tile, s0, ns;   // position on the line, block, column tile; this warp's first step and steps
     };
@@ -515,8 +519,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     if constexpr (!UP) grid_dependency_wait();   // h
     float* const red = reinterpret_cast<float*>(smem + roff);   // [wk][slot][TC]
     const uint32_t xoff = roff + values_at(RW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
-    float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));         // UP: [slot][block]
-    float* const ys = reinterpret_cast<float*>(smem + xoff);                                              // DOWN: [warp][T][TC]
+    // UP: x's steps, [slot][block]; DOWN: the sums of y, [warp][T][TC]
+    float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));
+    float* const ys = reinterpret_cast<float*>(smem + xoff);
     // This lane's 16-byte vectors of word row t (and t + 4): line r of 128 bytes holds them at chunk
     // cg ^ (r & 7).  UP: the lines of a word row's two halves follow each other; DOWN: 16 lines each.
     constexpr uint32_t HALF = UP ? 128u : STAGE / 2, LINE = UP ? 256u : 128u;   // to the other half, to the next row
@@ -652,7 +657,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 for (int n = 0; n < AT; ++n) {
 #pragma unroll
                     for (int j = 0; j < SPS; ++j)
-                        if (i + j < nq) bx[j][n] = *reinterpret_cast<const uint2*>(p.hq + hp[n] + (uint32_t)((i + j) * SK));
+                        if (i + j < nq)
+                            bx[j][n] = *reinterpret_cast<const uint2*>(p.hq + hp[n] + (uint32_t)((i + j) * SK));
                     if (i < nq) step_next[0][n] = p.hstep[hs[n] + i / xb];
                     if (SPS == 4 && xb == 2 && i + 2 < nq) step_next[1][n] = p.hstep[hs[n] + i / xb + 1];
                 }
@@ -663,7 +669,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             // as a float, that much more (128 * 255 * 128 < 2^22), so no conversion is needed.
             constexpr int BIAS = 0x4B400000;
             auto sum_value = [](int hi, int lo) {
-                const float2 v = unpack2(add2(pack2(__int_as_float(hi), __int_as_float(lo)), pack2(-12582912.0f, -12582912.0f)));
+                const float2 v =
+                    unpack2(add2(pack2(__int_as_float(hi), __int_as_float(lo)), pack2(-12582912.0f, -12582912.0f)));
                 return fmaf(256.0f, v.x, v.y);
             };
             auto clear = [&]() {
@@ -721,7 +728,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 }
             };
             // the block (or the group) ends: acc += s step (D - z X)
-            auto fold = [&](int i, int k, uint32_t sz) {   // k: the block's place in the stage; sz: the group's s row in it
+            // (k: the block's place in the stage; sz: the group's s row in it)
+            auto fold = [&](int i, int k, uint32_t sz) {
                 uint64_t step[AT], X[AT];   // twice each; X negated
 #pragma unroll
                 for (int n = 0; n < AT; ++n) {
@@ -786,7 +794,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                         if ((i + j) % xb == 0 || fresh) clear();
                         fresh = false;
                         mult(false, st, xi, j);
-                        if (--gleft == 0 || (i + j + 1) % xb == 0 || i + j + 1 == nq) fold(i + j, SPS == 4 && xb == 2 ? j / 2 : 0, sz);
+                        if (--gleft == 0 || (i + j + 1) % xb == 0 || i + j + 1 == nq)
+                            fold(i + j, SPS == 4 && xb == 2 ? j / 2 : 0, sz);
                         if (gleft == 0) {
                             gleft = p.spg;
                             fresh = true;
@@ -994,7 +1003,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             }
             return;
         }
-        // ---- the warps join their sums, then the tile's CTAs, each in their order; each CTA writes its share of the rows
+        // ---- the warps join their sums, then the tile's CTAs, each in their order; each CTA writes its share of y
         __syncthreads();
         for (int i = threadIdx.x; i < p.T * (TC / 4); i += MT) {
             float4 v = *reinterpret_cast<const float4*>(ys + 4 * i);
@@ -1046,12 +1055,12 @@ void cut_smem(Cut& c, bool up, int T, int S, int Q) {
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
 // leave room for (bt = 0: K is too long).
 //  * Few tokens, and no more tiles of 64 values of h than SMs: CTAs of 8 warps, beside which DOWN's start while
-//    they run (1 token, 8 experts of 2048 x 1024: 16.2 us against 19.7 us with 16; with 344 tiles, 2 experts of
-//    4096 x 11008, 59 us against 45 us).
+//    they run (1 token, 8 experts of 2048 x 1024: 14.6 us against 17.5 us with 16; with 344 tiles, 2 experts of
+//    4096 x 11008, 54 us against 41.5 us; 4 tokens, 32 experts of 2048 x 1024, 36.6 us against 30.2 us).
 //  * Else one CTA per SM and tiles of 128 values, 3 or 4 warps along K.  (Tiles of 64, where that fills the SMs' last
-//    round better, measured slower: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64 experts of 2048 x
-//    1024: 96 us against 81 us.  So did pairs of CTAs that halve the odd item of their part of the line: 48 tokens,
-//    8-bit, 99 us against 88 us; 1 token, 2 experts of 4096 x 11008, 40 us against 42 us.)
+//    round better, measured slower on an earlier form: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64
+//    experts of 2048 x 1024: 96 us against 81 us.  So did pairs of CTAs that halve the odd item of their part of the
+//    line: 48 tokens, 8-bit, 99 us against 88 us, though 1 token, 2 experts of 4096 x 11008, took 40 us against 42 us.)
 Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
     const int Q = (K + SK - 1) / SK;
     Cut c{};
