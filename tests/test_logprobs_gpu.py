@@ -245,3 +245,11 @@ def test_decode_step(cuda, libwq, M):
     for a, b in zip(eager[:4], captured[:4]):
         assert torch.equal(a, b)
     assert all(torch.equal(out[n], captured[4][n]) for n in out)
+
+
+@pytest.mark.parametrize("R,V", [(17, 16384), (20, 9000), (40, 9001), (100, 9000), (64, 50003), (128, 50000), (300, 49200)])
+def test_rows_split_over_ctas(cuda, libwq, R, V):
+    """Numbers of rows on both sides of every split of a row: 8, 4, 2 CTAs and one, and more CTAs than SMs."""
+    l, tok = draw(R, V, "bf16", R + V, cuda)
+    check(libwq, l, tok, 7)
+    assert libwq.device_status() == 0

@@ -261,6 +261,34 @@ assert torch.equal(y, plan(*a)) and wq.device_status() == 0
     assert r.returncode == 0, r.stdout + r.stderr
 
 
+def test_two_graphs_of_one_plan(cuda, libwq):
+    """More tokens than the warps keep sums for: two graphs of one plan, replayed at once on two streams, leave
+    their rows in workspaces of their own."""
+    import torch
+    p = moe_oracle.problem(24, 6, 3, 128, 352, 136, 8, 32, torch.bfloat16, seed=41)
+    ref, tol = moe_oracle.layer(p, 8, "silu")
+    (x, ids, weights), w = moe_oracle.to_gpu(libwq, p, 8, cuda)
+    plan = libwq.MoePlan(*w, 8, 32, 24, 3, pdl=True)
+    want = plan(x, ids, weights)
+    flipped = plan(x.flip(0).contiguous(), ids.flip(0).contiguous(), weights.flip(0).contiguous())
+    moe_oracle.assert_close(want, ref, tol)
+    runs = []
+    for a in ((x, ids, weights), (x.flip(0).contiguous(), ids.flip(0).contiguous(), weights.flip(0).contiguous())):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                y = plan(*a)
+        runs.append((g, y, a, torch.cuda.Stream()))
+    for _ in range(10):
+        for g, _, _, s in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(runs[0][1], want) and torch.equal(runs[1][1], flipped)
+    assert libwq.device_status() == 0
+
+
 def test_refusals(cuda, libwq):
     import torch
     p = moe_oracle.problem(2, 4, 2, 64, 32, 32, 4, 32, torch.float16, seed=1)
