@@ -120,6 +120,8 @@ def lib() -> ctypes.CDLL:
         L.wq_moe_route.restype = i
         L.wq_moe_workspace_size.argtypes = [i, i, i, i]
         L.wq_moe_workspace_size.restype = ctypes.c_size_t
+        L.wq_moe_selftest_smem.argtypes = [i] * 6 + [ctypes.POINTER(ctypes.c_size_t)]
+        L.wq_moe_selftest_smem.restype = ctypes.c_size_t
         L.wq_moe.argtypes = [p] * 10 + [i] * 9 + [u, p, ctypes.c_size_t, p]
         L.wq_moe.restype = i
         L.wq_logprobs.argtypes = [p, i, i, i, ctypes.c_int64, p, i, p, p, p, p, u, p]

@@ -309,6 +309,13 @@ size_t wq_moe_workspace_size(int T, int top_k, int inner, int N) {
     return wq::moe_workspace_bytes(T, top_k, inner, N);
 }
 
+size_t wq_moe_selftest_smem(int T, int top_k, int inner, int bits, int group_size, int cluster, size_t* used) {
+    if (!used || T < 1 || T > WQ_MOE_MAX_TOKENS || top_k < 1 || top_k > 16 || inner < 1 || (bits != 4 && bits != 8) ||
+        cluster < 1 || cluster > 8 || (group_size != -1 && (group_size < 32 || group_size % 32 != 0)))
+        return 0;
+    return wq::moe_down_smem(T, top_k, inner, bits, group_size, cluster, used);
+}
+
 wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* w_up,
                  const uint16_t* s_up, const uint16_t* z_up, const uint32_t* w_down, const uint16_t* s_down,
                  const uint16_t* z_down, uint16_t* y, int T, int K, int inner, int N, int E, int top_k, int bits,

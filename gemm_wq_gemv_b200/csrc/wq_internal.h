@@ -94,6 +94,7 @@ struct MoeProblem {
     void* ws;
 };
 size_t moe_workspace_bytes(int T, int top_k, int I, int N);
+size_t moe_down_smem(int T, int top_k, int I, int bits, int group_size, int cluster, size_t* used);
 wq_status launch_moe(const MoeProblem& m, cudaStream_t s);
 wq_status moe_device_status(int reset);
 

@@ -100,6 +100,11 @@ constexpr int up_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int down_warps(int nt) { return nt == 1 ? 8 : 6; }
 constexpr int along_k(int warps) { return warps == 12 ? 3 : 4; }   // warps of a CTA of UP along K
 constexpr uint64_t WAIT_NS = 2000000000ull;
+// DOWN, many tokens, at its end: the slots' tables, then up to PART_ROWS weighted rows of a tile's columns, in the
+// place of the rings (and beyond them: cut_smem counts the rows).
+constexpr int PART_AT = 8192, PART_ROWS = 192;
+__host__ __device__ constexpr int tokens_at_once(int top_k) { return PART_ROWS / top_k; }
+static_assert((8 * down_warps(2) + 1) * 4 + 3 * WQ_MOE_MAX_TOKENS * 16 * 2 <= PART_AT, "starts, place, first, last");
 
 template <int BITS> constexpr int step_rows() { return SK * BITS / 32; }   // word rows per step: 4 or 8
 
@@ -141,6 +146,13 @@ __device__ __forceinline__ void tma_load_3d_u32(uint32_t dst, const void* tmap, 
         "[%2];" ::"r"(dst),
         "l"(tmap), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
+}
+
+// Dynamic shared memory of this launch.
+__device__ __forceinline__ uint32_t dynamic_smem_bytes() {
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -951,8 +963,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             int16_t* const place = reinterpret_cast<int16_t*>(starts + 8 * MW + 1);  // S; then the first and the last warp
             int16_t* const wfirst = place + p.S;
             int16_t* const wlast = wfirst + p.S;
-            float* const part = reinterpret_cast<float*>(smem + 8192);               // [slots of a few tokens][TC]
-            constexpr int PART_ROWS = 192;
+            float* const part = reinterpret_cast<float*>(smem + PART_AT);            // [slots of a few tokens][TC]
+            const uint32_t part_at = smem_u32(part) - smem_u32(smem_raw);
             for (int i = threadIdx.x; i < p.S; i += MT) place[i] = -1;
             for (int w = threadIdx.x; w <= nw; w += MT) starts[w] = share(blk, Q4, w, nw);
             __syncthreads();
@@ -967,7 +979,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 }
             }
             __syncthreads();
-            const int step = PART_ROWS / p.top_k;   // tokens at a time
+            const int step = tokens_at_once(p.top_k);
             for (int k0 = 0; rank + k0 * p.cluster < p.T; k0 += step) {
                 const int nt = min(step, (p.T - rank - k0 * p.cluster + p.cluster - 1) / p.cluster);
                 for (int i = threadIdx.x; i < nt * p.top_k * (TC / 4); i += MT) {
@@ -989,7 +1001,8 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                         }
                         v = make_float4(a * v.x, a * v.y, a * v.z, a * v.w);
                     }
-                    *reinterpret_cast<float4*>(part + 4 * i) = v;
+                    if (check(part_at + 16u * i + 16u <= dynamic_smem_bytes(), &g_moe_status))
+                        *reinterpret_cast<float4*>(part + 4 * i) = v;
                 }
                 __syncthreads();
                 for (int i = threadIdx.x; i < nt * (TC / 4); i += MT) {
@@ -1045,11 +1058,17 @@ struct Cut {
     int xcol, nsteps, smem;
 };
 
+// DOWN with rows: the most that a CTA stages at a time, its tokens' slots.
+int staged_rows(int T, int top_k, int cluster) {
+    return std::min(tokens_at_once(top_k), (T + cluster - 1) / cluster) * top_k;
+}
+
 void cut_smem(Cut& c, bool up, int T, int S, int Q) {
     c.xcol = up ? xcol_bytes(Q) : 0;
     c.nsteps = up ? (Q + XBLK - 1) / XBLK : 0;
     c.smem = ring_bytes(c.W, c.sz_rows) + (up ? steps_at(c.W, c.bt, S, c.xcol) + c.bt * c.nsteps * 4
                                               : values_at(0, c.bt, S) + (c.rows ? 0 : c.W * T * MCOLS * 4));
+    if (!up && c.rows) c.smem = std::max(c.smem, 1024 + PART_AT + staged_rows(T, S / T, c.cluster) * MCOLS * 4);
 }
 
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
@@ -1113,30 +1132,36 @@ int clusters_that_fit(int cs) {
     return n;
 }
 
-// DOWN: a column tile is worked on by a cluster, of the size that leaves the fewest places of the SMs without a CTA:
-// two per SM, or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit
-// an empty device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
-Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
-    const int places = few ? sm_count() : 2 * sm_count();
+// DOWN with clusters of a given size.
+Cut cut_down(int T, int S, int I, int group_size, int bits, int cluster) {
     Cut c{};
     c.W = down_warps(T <= 4 ? 1 : 2);
     c.spg = group_size == -1 || group_size == I ? 1 << 29 : group_size / SK;
     c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
     c.bt = T <= 4 ? 4 : MAXBT;
+    c.cluster = cluster;
+    c.rows = T > SUMS_T;
+    cut_smem(c, false, T, S, 0);   // (at most 92 KB)
+    return c;
+}
+
+// DOWN: a column tile is worked on by a cluster, of the size that leaves the fewest places of the SMs without a CTA:
+// two per SM, or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit
+// an empty device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
+Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
+    const int places = few ? sm_count() : 2 * sm_count();
     const int tiles = (N + MCOLS - 1) / MCOLS;
-    int best = -1;   // places taken, in percent
+    int best = -1, cluster = 1;   // places taken, in percent
     for (int cs = 1; cs <= 8; ++cs) {
         const int held = clusters_that_fit(cs), all = held - (cs > 1 ? (held + 15) / 16 : 0);
         const int fit = std::max(1, few ? all / 2 : all);
         const int waves = (tiles + fit - 1) / fit, use = (int)(100ll * tiles * cs / ((long long)waves * places));
         if (use > best + 2) {
             best = use;
-            c.cluster = cs;
+            cluster = cs;
         }
     }
-    c.rows = T > SUMS_T;
-    cut_smem(c, false, T, S, 0);   // (at most 92 KB)
-    return c;
+    return cut_down(T, S, I, group_size, bits, cluster);
 }
 
 template <int BITS, bool BF, int NT, bool UP, int W>
@@ -1257,6 +1282,16 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
 size_t moe_workspace_bytes(int T, int top_k, int I, int N) {
     const size_t tiles = (N + MCOLS - 1) / MCOLS, rows = (size_t)T * top_k + MAXBT * 64;   // 64 warps in the largest cluster
     return h_bytes(T * top_k, I) + (T > SUMS_T ? tiles * rows * MCOLS * 4 : 0);
+}
+
+// What DOWN asks for with clusters of the given size, and the end of what it touches (the round-up of the rings to 1024
+// bytes among it).
+size_t moe_down_smem(int T, int top_k, int I, int bits, int group_size, int cluster, size_t* used) {
+    const Cut c = cut_down(T, T * top_k, I, group_size, bits, cluster);
+    const int tables = ring_bytes(c.W, c.sz_rows) - 1 + values_at(0, c.bt, T * top_k);
+    *used = c.rows ? std::max(tables, 1023 + PART_AT + staged_rows(T, top_k, cluster) * MCOLS * 4)
+                   : tables + c.W * T * MCOLS * 4;
+    return c.smem;
 }
 
 wq_status launch_moe(const MoeProblem& m, cudaStream_t stream) {

@@ -503,6 +503,14 @@ int wq_checked_build(void);
  */
 wq_status wq_selftest_wait_timeout(uint64_t limit_ns, void* stream);
 
+/*
+ * Host-only self-test of wq_moe's launch arithmetic: the dynamic shared memory,
+ * in bytes, that its second product asks for with `cluster` (1 to 8) CTAs per
+ * tile of columns, and in *used the end of what a CTA touches of it at most.
+ * 0 for arguments that wq_moe refuses.
+ */
+size_t wq_moe_selftest_smem(int T, int top_k, int inner, int bits, int group_size, int cluster, size_t* used);
+
 #ifdef __cplusplus
 }
 #endif
