@@ -337,7 +337,7 @@ wq_status wq_moe(const uint16_t* x, const int32_t* ids, const float* weights, co
         if (group_size % 32 != 0) return WQ_ERR_UNSUPPORTED;
     }
     if (K > WQ_MOE_MAX_K) return WQ_ERR_UNSUPPORTED;
-    // (the kernel finds a slot's h, two bytes per value, by a 32-bit offset)
+    // (the kernel finds a slot's h, three bytes per value, by a 32-bit offset: 3 * 2^30 and the rows' padding fit)
     if (2ll * T * top_k * ((inner + 31) / 32 * 32) >= 1ll << 31) return WQ_ERR_UNSUPPORTED;
     if (inner % 8 != 0 || N % 8 != 0) return WQ_ERR_ALIGNMENT;
     if (!aligned(x, 16) || !aligned(w_up, 16) || !aligned(s_up, 16) || !aligned(z_up, 16) || !aligned(w_down, 16) ||

@@ -31,22 +31,27 @@
 //    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
 //    bytes with 3 instructions per word, 8-bit codes are used as they are, and
 //    m16n8k32 on u8 x s8 (2.1 clocks too, twice the work) sums them exactly in int32.
-//  * x (or h) becomes 16-bit fixed point: per token and block of 128 values
-//    (aligned in K) a power-of-two step that puts the largest value at 2^14 to
-//    2^15, held as two signed bytes, which are two adjacent columns of the MMA:
-//    x = step * (256 hi + lo).  Error: half a step, at most 2^-15 of the block's
-//    largest value, none for values whose own last bit is at or above the step
-//    (a bf16 within 2^-7 of the largest, an fp16 within 2^-4); random over the
-//    block, so a product moves by about 3e-5 of itself, a tenth of the rounding of
-//    an fp16 output.  UP converts x once per block of slots, while its first words
-//    arrive, and leaves h converted (a tile's 128 values of a slot, or 64, are one
-//    block), so that DOWN only reads bytes.  A block with a value that is not finite
-//    gets the step NaN.
-//  * One more MMA per step with A = 1 gives X, the tokens' sums, so that a zero
-//    point of any value costs nothing per code.  At the end of a block (or group):
-//    acc += s * step * (D - z X) in fp32, D = 256 D_hi + D_lo.
-//  * Loads.  A warp's words come by TMA, 16 word rows x 64 columns per stage (4 KB)
-//    with the s and z rows of its groups, into a private ring of two stages: 96 to
+//  * x (or h) becomes 24-bit fixed point: per token and block of 128 values
+//    (aligned in K; 64 where UP's tiles are) a power-of-two step that puts the largest
+//    value at 2^22 to 2^23, held as three signed bytes, x = step * (256 (256 hi + mid) +
+//    lo).  Error: half a step, at most 1.02 * 2^-23 of the block's largest value, which is
+//    what fp32 sums lose to a value of that size; none for values whose own last bit is at
+//    or above the step (a bf16 within 2^-15 of the largest, an fp16 within 2^-12).  (Two
+//    bytes were not enough: next to a value 3000 times the rest of its block, as single
+//    channels have them, the rest kept 4 %, and where that value's codes lie at z it is
+//    the rest that is the output.)  hi and mid of a slot are two adjacent columns of the
+//    MMA, the lo of all slots a tile of their own.  UP converts x once per block of slots,
+//    while its first words arrive, and leaves h converted (a tile's 128 values of a slot,
+//    or 64, are one block), so that DOWN only reads bytes.  A block with a value that is
+//    not finite gets the step NaN.
+//  * The sums X of the values, which a zero point of any value needs, are taken when they
+//    are converted, per unit: the 1, 2 or 4 steps of 32, as many as a group and a block
+//    hold.  At the end of a unit: acc += s * step * (D - z X) in fp32,
+//    D = 256 (256 D_hi + D_mid) + D_lo.  The unit's length is a template parameter: with
+//    all three in one kernel, and a path for the rest of K, registers spilled and 16
+//    tokens took 160 us instead of 128.
+//  * Loads.  A warp's words come by TMA, 128 values of K x 64 columns (8-bit: 32, the
+//    halves in turn) per stage (4 KB) with the s and z rows of its groups, into a private ring of two stages: 96 to
 //    128 KB in flight per SM.  The 128-byte swizzle and the column order of the lanes
 //    (chunk cg) keep the 16-byte reads free of bank conflicts.  (cp.async by every
 //    lane, which this replaced, cost 19 instructions per step of 32 values, a quarter
@@ -88,8 +93,13 @@ constexpr int MAXBT = 8;        // slots per block
 constexpr int SUMS_T = 16;
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
-constexpr int BOX_ROWS = 16;    // word rows per TMA box
-constexpr int STAGE = 2 * BOX_ROWS * 128;   // bytes: two halves
+// A stage: 4 KB of words.  4-bit: 16 word rows (128 values of K) of both halves; 8-bit: 32 (128 again) of one half, the
+// halves in turn.  So a block of fixed-point values is multiplied with one half of the columns after the other, and the
+// sums of one half alone are in registers.
+constexpr int STAGE = 4096;
+template <int BITS> constexpr int stage_rows() { return BITS == 4 ? 16 : 32; }
+// Space for a stage's s rows and its z rows (64 or 32 columns), each at a multiple of 128 bytes.
+__host__ __device__ constexpr int sz_space(int bits, int rows) { return bits == 4 ? 256 * rows : (rows + 1) / 2 * 256; }
 constexpr int NST = 2;          // ring stages per warp (DOWN with 3: the same time)
 // Warps of a CTA with NT token tiles.  Two tiles need about 160 registers: with 16 warps per SM, and 128, the spilled
 // ones passed through L2, shared memory leaving little L1.  So 12 per SM, UP 12 in one CTA, DOWN 6 in each of two
@@ -110,13 +120,16 @@ template <int BITS> constexpr int step_rows() { return SK * BITS / 32; }   // wo
 
 struct MoeParams {
     const uint16_t* x;      // UP: (T, K)
-    int8_t* hq;             // (S, 2, Qh * SK): h in fixed point, hi then lo bytes, in the byte order of DOWN's MMA
-    float* hstep;           // (S, Qh): its steps, one per hb steps of K
+    int8_t* hq;             // (S, 3, Qh * SK): h in fixed point, hi, mid and lo bytes, in the byte order of DOWN's MMA
+    // (S, Qh >> hlog): its units, the sum of the values and the step's bits.  A unit is the 1, 2 or 4 steps, as many as
+    // no group ends inside, of a block of fixed-point values.
+    uint2* hunit;
     const int32_t* ids;     // (T, top_k)
     const float* weights;   // (T, top_k)
     uint16_t* y;            // (T, N)
     float* rows;            // DOWN, many tokens: (tiles, S + bt * warps of a cluster, 64), the items' rows; else NULL
     int T, top_k, S, E, bt; // bt: slots per block
+    int nblk;               // most blocks there can be
     int K;                  // inner length of this product (UP: K of x, DOWN: I)
     int NW;                 // weight columns (UP: 2 I, DOWN: N)
     int I;
@@ -127,8 +140,8 @@ struct MoeParams {
     int sz_rows;            // s (and z) rows per stage
     int act;
     int xcol;               // UP: bytes between two columns of x's fixed-point values
-    int nsteps;             // UP: fixed-point blocks of x
-    int Qh, hb;             // steps of K in a row of h; steps of K per fixed-point block of h (4 or 2)
+    int nunits;             // UP: units of x
+    int Qh, hlog;           // steps of K in a row of h (whole stages); steps per unit of h, log2
     int cluster;            // DOWN: CTAs per column tile
 };
 
@@ -216,9 +229,12 @@ struct Blocks {         // in shared memory
     // slots of block u
     __device__ __forceinline__ int count(int u) const { return first[u + 1] - first[u]; }
 };
-__host__ __device__ constexpr int table_slots(int S) { return S < 32 ? 32 : S; }
-__host__ __device__ constexpr int table_bytes(int S) {
-    return ((table_slots(S) + 1) * 4 + (3 * table_slots(S) + 1) * 2 + 15) / 16 * 16;
+// More blocks than these cannot be: e experts with m slots each take the sum of ceil(m / bt) <= (S + e (bt - 1)) / bt.
+__host__ __device__ constexpr int most_blocks(int S, int E, int bt) {
+    return (S + (E < S ? E : S) * (bt - 1)) / bt;
+}
+__host__ __device__ constexpr int table_bytes(int S, int nblk) {
+    return ((nblk + 1) * 4 + (2 * nblk + 1 + S) * 2 + 15) / 16 * 16;
 }
 
 // Weight of a block of m slots: two token tiles take more instructions, the same loads.  (16 tokens, 2 of 8 experts,
@@ -363,46 +379,64 @@ __device__ __forceinline__ float activate(float g, int act) {
     return 0.5f * g * erfcf(-0.70710678118654752f * g);  // gelu
 }
 
-// 8 values as 16-bit fixed point with step 2^(E - 141), `inv` = 2^(141 - E): the sum with
-// 1.5 * 2^23 + 128 rounds to an integer whose low 16 bits are x + 128; its second byte is
-// hi, its first, with the top bit flipped, lo: x = 256 hi + lo, both in -128 .. 127.
+// 8 values as 24-bit fixed point with step 2^(E - 149), `inv` = 2^(149 - E): the integer plus 0x808080 has the bytes
+// hi, mid and lo plus 128: x = 256^2 hi + 256 mid + lo, all in -128 .. 127.
 // Byte order: 4-bit words, the codes 0 2 4 6 and 1 3 5 7 of a word row; 8-bit, as they come.
+struct Bytes {
+    uint2 hi, mid, lo;
+};
 template <int BITS>
-__device__ __forceinline__ void to_fixed(const float (&v)[8], float inv, uint2& hi, uint2& lo) {
+__device__ __forceinline__ Bytes to_fixed(const float (&v)[8], float inv) {
     uint32_t u[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(fmaf(v[i], inv, 12582912.0f + 128.0f));
-    auto four = [&](int a, int b, int c, int d, uint32_t& h, uint32_t& l) {
+    for (int i = 0; i < 8; ++i) u[i] = (uint32_t)__float2int_rn(v[i] * inv) + 0x808080u;
+    auto four = [&](int a, int b, int c, int d, uint32_t& h, uint32_t& m, uint32_t& l) {
         const uint32_t p = prmt(u[a], u[b], 0x5140u), q = prmt(u[c], u[d], 0x5140u);  // bytes a0 b0 a1 b1
         l = prmt(p, q, 0x5410u) ^ 0x80808080u;
-        h = prmt(p, q, 0x7632u);
+        m = prmt(p, q, 0x7632u) ^ 0x80808080u;
+        h = prmt(prmt(u[a], u[b], 0x0062u), prmt(u[c], u[d], 0x0062u), 0x5410u) ^ 0x80808080u;
     };
+    Bytes r;
     if constexpr (BITS == 4) {
-        four(0, 2, 4, 6, hi.x, lo.x);
-        four(1, 3, 5, 7, hi.y, lo.y);
+        four(0, 2, 4, 6, r.hi.x, r.mid.x, r.lo.x);
+        four(1, 3, 5, 7, r.hi.y, r.mid.y, r.lo.y);
     } else {
-        four(0, 1, 2, 3, hi.x, lo.x);
-        four(4, 5, 6, 7, hi.y, lo.y);
+        four(0, 1, 2, 3, r.hi.x, r.mid.x, r.lo.x);
+        four(4, 5, 6, 7, r.hi.y, r.mid.y, r.lo.y);
     }
+    return r;
 }
 
-// Exponent E of a block whose largest magnitude has the bits `top`: |x| 2^(141 - E) <= 32512 (127 * 256), one more
-// from 1.984 * 2^n up; and its step 2^(E - 141), NaN where a value is not finite.
+// Exponent E of a block whose largest magnitude has the bits `top`: |x| 2^(149 - E) <= 1.984375 * 2^22 < 0x7F7F80, one
+// more from 1.984375 * 2^n up (at least 23: a step is no subnormal); and its step 2^(E - 149), NaN where a value is not
+// finite.
 __device__ __forceinline__ uint32_t block_exponent(uint32_t top) {
-    return min(max((top + 0x00020000u) >> 23, 15u), 255u);
+    return min(max((top + 0x00020000u) >> 23, 23u), 255u);
 }
-__device__ __forceinline__ float block_step(uint32_t top, uint32_t E) {
-    return top >= 0x7F800000u ? NAN : __uint_as_float((E - 14u) << 23);
+__device__ __forceinline__ float block_inverse(uint32_t E) { return __uint_as_float((276u - E) << 23); }
+__device__ __forceinline__ uint32_t block_step(uint32_t top, uint32_t E) {
+    return top >= 0x7F800000u ? 0x7FC00000u : (E - 22u) << 23;
 }
 
-// Shared memory behind the rings: the warps' partials, the blocks; UP: x's fixed-point values and their steps; DOWN:
+// The sum of 8 values, from their bytes.
+__device__ __forceinline__ int value_sum(const Bytes& b) {
+    auto sum = [](uint2 v) { return __dp4a((int)v.y, 0x01010101, __dp4a((int)v.x, 0x01010101, 0)); };
+    return 256 * (256 * sum(b.hi) + sum(b.mid)) + sum(b.lo);
+}
+
+// Shared memory behind the rings: the warps' partials, the blocks; UP: x's fixed-point values and their units; DOWN:
 // the sums of y.
 __host__ __device__ constexpr int table_at(int W, int bt) { return W * bt * MCOLS * 4; }
-__host__ __device__ constexpr int values_at(int W, int bt, int S) { return table_at(W, bt) + table_bytes(S); }
-__host__ __device__ constexpr int steps_at(int W, int bt, int S, int xcol) { return values_at(W, bt, S) + 2 * bt * xcol; }
+__host__ __device__ constexpr int values_at(int W, int bt, int S, int nblk) {
+    return table_at(W, bt) + table_bytes(S, nblk);
+}
+__host__ __device__ constexpr int units_at(int W, int bt, int S, int nblk, int xcol) {
+    return values_at(W, bt, S, nblk) + 3 * bt * xcol;
+}
 
-// NT: token tiles of 4 slots (8 MMA columns).  MW: warps.
-template <int BITS, bool BF, int NT, bool UP, int MW>
+// NT: token tiles of 4 slots (8 MMA columns).  MW: warps.  U: steps per unit (XBLK but for groups that are no multiple of
+// 128, and for blocks of h of 64 values).
+template <int BITS, bool BF, int NT, bool UP, int MW, int U>
 __global__ void __launch_bounds__(MW * 32, UP ? 16 / MW : 2)
 moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_s,
            const __grid_constant__ CUtensorMap tm_z, const MoeParams p) {
@@ -410,7 +444,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     using T16 = Dt<BF>;
     constexpr int RPS = step_rows<BITS>();       // 4 or 8
     constexpr int RL = RPS / 4;                  // word rows per lane and step
-    constexpr int SPS = BOX_ROWS / RPS;          // steps per stage
+    constexpr int SPS = XBLK;                    // steps per stage
     constexpr int WK = UP ? along_k(MW) : 1;               // UP: warps along K
     constexpr int WC = UP ? MW / WK : 1;         // and along the columns.  DOWN: every warp works alone
     constexpr int TC = MCOLS * WC;               // weight columns per tile
@@ -424,7 +458,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const int g = lane >> 2, t = lane & 3;
     // 16-byte column chunk of this lane (columns 4 cg .. 4 cg + 3 of each half): with the lines of a
     // stage below, the eight lanes of a quarter-warp meet eight different bank groups
-    const int cg = UP ? g : ((g & 1) << 2) | (g >> 1);
+    const int cg = UP && BITS == 4 ? g : ((g & 1) << 2) | (g >> 1);
     const int wk = warp / WC, wc = warp % WC;   // UP
     uint64_t* const bar = bars + warp * NST;
     if (lane == 0) {
@@ -439,13 +473,12 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     grid_launch_dependents();
     const int Q4 = (p.Q + XBLK - 1) / XBLK;
     const int rank = UP ? 0 : (int)blockIdx.x % p.cluster;
-    const uint32_t sz_bytes = 256u * (uint32_t)p.sz_rows;   // a stage's s rows, then its z rows
+    const uint32_t sz_bytes = sz_space(BITS, p.sz_rows);    // a stage's s rows, then its z rows
     const uint32_t roff = MW * NST * (STAGE + sz_bytes);    // behind the rings
     constexpr int RW = UP ? MW : 0;   // warps with partials in shared memory
     uint8_t* const tab = smem + roff + table_at(RW, p.bt);
-    const int ts = table_slots(p.S);
-    int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (ts + 1));
-    const Blocks blk{&nblocks, reinterpret_cast<int*>(tab), tab16, tab16 + ts, tab16 + 2 * ts + 1};
+    int16_t* const tab16 = reinterpret_cast<int16_t*>(tab + 4 * (p.nblk + 1));
+    const Blocks blk{&nblocks, reinterpret_cast<int*>(tab), tab16, tab16 + p.nblk, tab16 + 2 * p.nblk + 1};
     find_blocks<MT>(p, blk, reinterpret_cast<int*>(smem));
     // this CTA's part of the line (UP) or this warp's (DOWN): lane 0 finds where it starts, the others where it ends
     const int part = UP ? (int)blockIdx.x : rank * MW + warp, parts = UP ? (int)gridDim.x : p.cluster * MW;
@@ -490,7 +523,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     const uint32_t sz_ring = smem_u32(smem) + MW * NST * STAGE + (uint32_t)warp * (NST * sz_bytes);
     Item wit = it;                          // the item whose stages are being requested
     const int g0 = it.s0 / p.spg, gp0 = it.s0 - g0 * p.spg;   // UP: of every item; DOWN: of the first, then 0
-    int wleft = 0;                          // stages left in it
+    int wleft = 0, whalf = 0;               // stages left in it; 8-bit: the half of the next one
     int row = 0, grow = 0, gpos = 0;        // the next stage: word row, s row, steps into its group
     bool ok = true, first = true;
     auto issue = [&](uint32_t slot) {
@@ -498,7 +531,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             // (an item of UP has no steps for a warp past the end of K: nor has any other)
             if (!first) next(wit);
             if (wit.at >= end || wit.ns == 0) return;
-            wleft = (wit.ns + SPS - 1) / SPS;
+            wleft = (wit.ns + SPS - 1) / SPS * (BITS == 4 ? 1 : 2);
             const int e = blk.e[wit.u];
             row = e * p.Kw + wit.s0 * RPS;
             grow = e * p.groups + (UP || first ? g0 : 0);
@@ -507,42 +540,48 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         }
         if (lane == 0) {
             uint64_t* const b = &bar[slot];
-            mbar_arrive_expect_tx(b, STAGE + sz_bytes);
+            mbar_arrive_expect_tx(b, STAGE + (BITS == 4 ? 256u : 128u) * (uint32_t)p.sz_rows);
             const int wcol = col(wit.tile);
             const uint32_t dst = ring + slot * STAGE, sz = sz_ring + slot * sz_bytes;
             if constexpr (UP) {
-                tma_load_3d_u32(dst, &tm, b, wcol, 0, row);
-                tma_load_3d_u32(sz, &tm_s, b, wcol, 0, grow);
-                tma_load_3d_u32(sz + sz_bytes / 2, &tm_z, b, wcol, 0, grow);
+                tma_load_3d_u32(dst, &tm, b, wcol, whalf, row);
+                tma_load_3d_u32(sz, &tm_s, b, wcol, whalf, grow);
+                tma_load_3d_u32(sz + sz_bytes / 2, &tm_z, b, wcol, whalf, grow);
             } else {
-                tma_load_2d_u32(dst, &tm, b, wcol, row);
-                tma_load_2d_u32(dst + STAGE / 2, &tm, b, wcol + 32, row);
-                tma_load_2d_u32(sz, &tm_s, b, wcol, grow);
-                tma_load_2d_u32(sz + sz_bytes / 2, &tm_z, b, wcol, grow);
+                tma_load_2d_u32(dst, &tm, b, wcol + 32 * whalf, row);
+                if constexpr (BITS == 4) tma_load_2d_u32(dst + STAGE / 2, &tm, b, wcol + 32, row);
+                tma_load_2d_u32(sz, &tm_s, b, wcol + 32 * whalf, grow);
+                tma_load_2d_u32(sz + sz_bytes / 2, &tm_z, b, wcol + 32 * whalf, grow);
             }
         }
-        row += BOX_ROWS;
-        for (gpos += SPS; gpos >= p.spg; gpos -= p.spg) ++grow;
         --wleft;
+        if constexpr (BITS == 8) {
+            whalf ^= 1;
+            if (whalf) return;
+        }
+        row += stage_rows<BITS>();
+        for (gpos += SPS; gpos >= p.spg; gpos -= p.spg) ++grow;
     };
     issue(0);
     issue(1);
 
     if constexpr (!UP) grid_dependency_wait();   // h
     float* const red = reinterpret_cast<float*>(smem + roff);   // [wk][slot][TC]
-    const uint32_t xoff = roff + values_at(RW, p.bt, p.S), xbase = smem_u32(smem) + xoff;                  // UP
-    // UP: x's steps, [slot][block]; DOWN: the sums of y, [warp][T][TC]
-    float* const steps = reinterpret_cast<float*>(smem + roff + steps_at(MW, p.bt, p.S, p.xcol));
+    const uint32_t xoff = roff + values_at(RW, p.bt, p.S, p.nblk), xbase = smem_u32(smem) + xoff;          // UP
+    // UP: x's units, [slot][unit]; DOWN: the sums of y, [warp][T][TC]
+    uint2* const units = reinterpret_cast<uint2*>(smem + roff + units_at(MW, p.bt, p.S, p.nblk, p.xcol));
     float* const ys = reinterpret_cast<float*>(smem + xoff);
     // This lane's 16-byte vectors of word row t (and t + 4): line r of 128 bytes holds them at chunk
-    // cg ^ (r & 7).  UP: the lines of a word row's two halves follow each other; DOWN: 16 lines each.
-    constexpr uint32_t HALF = UP ? 128u : STAGE / 2, LINE = UP ? 256u : 128u;   // to the other half, to the next row
-    // (UP: rows 4 apart have the same swizzle; DOWN: the two halves have)
-    const uint32_t off0 = t * LINE + (((uint32_t)cg ^ ((UP ? 2 * t : t) & 7u)) << 4);
-    const uint32_t off1 = UP ? t * LINE + HALF + (((uint32_t)cg ^ ((2 * t + 1) & 7u)) << 4)
-                             : (t + 4) * LINE + (((uint32_t)cg ^ (t + 4u)) << 4);
+    // cg ^ (r & 7).  4-bit UP: the lines of a word row's two halves follow each other; 4-bit DOWN: 16 lines each.
+    constexpr bool PAIRED = UP && BITS == 4;
+    constexpr uint32_t HALF = PAIRED ? 128u : BITS == 4 ? STAGE / 2 : 0u;   // to the other half
+    constexpr uint32_t LINE = PAIRED ? 256u : 128u;                          // to the next row
+    // (paired: rows 4 apart have the same swizzle; else: the two halves have)
+    const uint32_t off0 = t * LINE + (((uint32_t)cg ^ ((PAIRED ? 2 * t : t) & 7u)) << 4);
+    const uint32_t off1 = PAIRED ? t * LINE + HALF + (((uint32_t)cg ^ ((2 * t + 1) & 7u)) << 4)
+                                 : (t + 4) * LINE + (((uint32_t)cg ^ (t + 4u)) << 4);
     auto off = [&](int odd, int hf) {   // constants
-        if constexpr (UP) return (hf ? off1 : off0) + 4 * LINE * odd;
+        if constexpr (PAIRED) return (hf ? off1 : off0) + 4 * LINE * odd;
         else return (odd ? off1 : off0) + HALF * hf;
     };
     uint32_t slot = 0, phase = 0;   // ring position of the next stage to read
@@ -557,6 +596,9 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             __syncwarp();
         }
 
+    // UP: the column of slot m's lo bytes (full blocks: the four that a load phase reads, slots 0 4 1 5 and 2 6 3 7, lie
+    // in different banks)
+    auto lo_col = [&](int m) { return 2 * p.bt + (p.bt == 8 ? m ^ ((m >> 1) & 2) : m); };
     int block = -1;   // UP: the block whose values are in shared memory
     int done = 0;     // items finished
     for (; it.at < end; next(it)) {
@@ -565,7 +607,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
         const int bm = blk.count(it.u);
         if (UP && it.u != block) {
             // ---- another block: x of its slots as fixed point.  Column 2 m holds hi of the block's slot m, 2 m + 1
-            // its lo: 32 bytes per step, 8 for each word row t.
+            // its mid, and lo_col(m) its lo: 32 bytes per step, 8 for each word row t.
             block = it.u;
             // (the previous block's were last read before the barrier behind the partials)
             // (slot, 8 steps) pairs of this warp, XU at a time so that their loads overlap; a lane has 8 values
@@ -583,7 +625,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                     raw[u] = make_uint4(0u, 0u, 0u, 0u);
                     const uint16_t* const src = p.x + (size_t)(slot / p.top_k) * p.K + k;
                     if constexpr (BITS == 4) {                // K is a multiple of 8
-                        if (in && k < p.K) raw[u] = *reinterpret_cast<const uint4*>(src);
+                        if (in && k < p.K) raw[u] = *reinterpret_cast<const uint4*>(src);   // (else 0)
                     } else {                                  // K is a multiple of 4
                         uint2 a = make_uint2(0u, 0u), c = a;
                         if (in && k < p.K) a = *reinterpret_cast<const uint2*>(src);
@@ -595,7 +637,7 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
                 for (int u = 0; u < XU; ++u) {
                     if (p0 + u >= pairs) break;
                     const int pr = p0 + u, m = wc + pr / rounds * WC, qo = pr % rounds * 8 + g, q = q0 + qo;
-                    const bool in = qo < nq;
+                    const bool in = qo < (nq + U - 1) / U * U;   // the last unit is filled up with zeros
                     float v[8];
                     const uint32_t r0[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
 #pragma unroll
@@ -610,23 +652,30 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
 #pragma unroll
                     for (int d = 8; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
                     const uint32_t E = block_exponent(top);
-                    uint2 hi, lo;
-                    to_fixed<BITS>(v, __uint_as_float((268u - E) << 23), hi, lo);
+                    const Bytes b = to_fixed<BITS>(v, block_inverse(E));
                     const uint32_t at = xbase + (uint32_t)(2 * m) * p.xcol + (uint32_t)q * 32u;
-                    if (in && check(q * 32 + 32 <= p.xcol, &g_moe_status)) {
+                    const uint32_t at_lo = xbase + (uint32_t)lo_col(m) * p.xcol + (uint32_t)q * 32u;
+                    if (in && check(q * 32 + 32 <= p.xcol && lo_col(m) < 3 * p.bt, &g_moe_status)) {
                         if constexpr (BITS == 4) {
-                            sts64(at + 8u * t, hi.x, hi.y);
-                            sts64(at + p.xcol + 8u * t, lo.x, lo.y);
+                            sts64(at + 8u * t, b.hi.x, b.hi.y);
+                            sts64(at + p.xcol + 8u * t, b.mid.x, b.mid.y);
+                            sts64(at_lo + 8u * t, b.lo.x, b.lo.y);
                         } else {   // word row j of the step (4 values each): bytes 8 (j % 4) + 4 (j / 4)
                             const uint32_t j = 2u * t, o = 8u * (j & 3u) + 4u * (j >> 2);
-                            sts32(at + o, hi.x);
-                            sts32(at + o + 8u, hi.y);
-                            sts32(at + p.xcol + o, lo.x);
-                            sts32(at + p.xcol + o + 8u, lo.y);
+                            sts32(at + o, b.hi.x);
+                            sts32(at + o + 8u, b.hi.y);
+                            sts32(at + p.xcol + o, b.mid.x);
+                            sts32(at + p.xcol + o + 8u, b.mid.y);
+                            sts32(at_lo + o, b.lo.x);
+                            sts32(at_lo + o + 8u, b.lo.y);
                         }
                     }
-                    if ((lane & 15) == 0 && in && check(q / XBLK < p.nsteps, &g_moe_status))
-                        steps[m * p.nsteps + q / XBLK] = block_step(top, E);
+                    int sum = value_sum(b);   // of the lane, its step (4 lanes) and its unit (4, 8 or 16)
+#pragma unroll
+                    for (int d = 1; d < 16; d <<= 1)
+                        if (d < 4 * U) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    if (lane % (4 * U) == 0 && in && check(q / U < p.nunits, &g_moe_status))
+                        units[m * p.nunits + q / U] = make_uint2((uint32_t)sum, block_step(top, E));
                 }
             }
             __syncthreads();
@@ -640,186 +689,190 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
             for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                 for (int n = 0; n < AT; ++n) acc[hf][0][n] = acc[hf][1][n] = 0ull;
-            // B column g of token tile n: UP from shared memory; DOWN straight from global memory, a stage ahead (every
-            // CTA reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
-            uint32_t xa[AT], sp[AT];               // UP
-            uint32_t hp[AT], hs[AT];               // DOWN: offsets of values and steps (wq_moe refuses 2^31 bytes)
-            uint2 bx[SPS][AT];
-            float step_next[2][AT];
+            // B column g of token tile n: hi and mid of slots 4 n + g / 2; of the last one, lo of slots g / 2 (g even)
+            // and 4 + g / 2 (odd).  UP from shared memory; DOWN straight from global memory, a stage ahead (every CTA
+            // reads the same bytes: L2).  Columns beyond the block's slots: any bytes, the results are not used.
+            uint32_t at[AT + 1], unit[AT];         // offsets of values and units
+            [[maybe_unused]] uint2 ux[AT];
+            uint2 bx[SPS][AT + 1];                 // this stage's values; DOWN: its units, that of step g % 4
             [[maybe_unused]] float wt[AT];         // DOWN: weights of the slots 4 n + t and their rows of y's sums
             [[maybe_unused]] uint32_t yrow[AT];
-            const int xb = UP ? XBLK : p.hb;       // steps per fixed-point block: XBLK, or 2
+            const int third = (g >> 1) + (AT > 1 ? 4 * (g & 1) : 0);
 #pragma unroll
             for (int n = 0; n < AT; ++n) {
                 if constexpr (UP) {
-                    xa[n] = xoff + (uint32_t)min(8 * n + g, 2 * p.bt - 1) * p.xcol + (uint32_t)q0 * 32u + 8u * t;
-                    sp[n] = smem_u32(steps + min(4 * n + t, p.bt - 1) * p.nsteps + q0 / XBLK);
+                    at[n] = xoff + (uint32_t)min(8 * n + g, 2 * p.bt - 1) * p.xcol + (uint32_t)q0 * 32u + 8u * t;
+                    unit[n] = smem_u32(units + min(4 * n + t, p.bt - 1) * p.nunits + q0 / U);
                 } else {
-                    const int col = 2 * slots[min(4 * n + (g >> 1), bm - 1)] + (g & 1);
-                    hp[n] = (uint32_t)(col * p.Qh + q0) * SK + 8 * t;
+                    const int col = 3 * slots[min(4 * n + (g >> 1), bm - 1)] + (g & 1);
+                    at[n] = (uint32_t)(col * p.Qh + q0) * SK + 8 * t;   // (wq_moe keeps it below 3 * 2^30)
                     const int sl = slots[min(4 * n + t, bm - 1)];
-                    hs[n] = sl * p.Qh + q0 / xb;
+                    unit[n] = (sl * p.Qh + q0) / U;         // (Qh is a multiple of XBLK)
                     wt[n] = p.weights[sl];
                     yrow[n] = (uint32_t)(warp * p.T + sl / p.top_k) * TC + 4 * cg;
-                    check(col < 2 * p.S, &g_moe_status);
+                    check(col < 3 * p.S, &g_moe_status);
                 }
             }
-            auto request = [&](int i) {            // DOWN: the values of the stage from step i, and its blocks' steps
+            at[AT] = UP ? xoff + (uint32_t)lo_col(min(third, p.bt - 1)) * p.xcol + (uint32_t)q0 * 32u + 8u * t
+                        : (uint32_t)((3 * slots[min(third, bm - 1)] + 2) * p.Qh + q0) * SK + 8 * t;
+            auto request = [&](int i) {            // the values of the stage from step i; DOWN: and its units
 #pragma unroll
-                for (int n = 0; n < AT; ++n) {
+                for (int j = 0; j < SPS; ++j)
 #pragma unroll
-                    for (int j = 0; j < SPS; ++j)
-                        if (i + j < nq)
-                            bx[j][n] = *reinterpret_cast<const uint2*>(p.hq + hp[n] + (uint32_t)((i + j) * SK));
-                    if (i < nq) step_next[0][n] = p.hstep[hs[n] + i / xb];
-                    if (SPS == 4 && xb == 2 && i + 2 < nq) step_next[1][n] = p.hstep[hs[n] + i / xb + 1];
+                    for (int n = 0; n <= AT; ++n)
+                        bx[j][n] = UP ? *reinterpret_cast<const uint2*>(smem + at[n] + 32 * (i + j))
+                                      : *reinterpret_cast<const uint2*>(p.hq + at[n] + (uint32_t)((i + j) * SK));
+                if constexpr (!UP) {
+#pragma unroll
+                    for (int n = 0; n < AT; ++n) ux[n] = p.hunit[unit[n] + (i + (g & (SPS - 1))) / U];
                 }
             };
-            if constexpr (!UP) request(0);
-            int d[2][2][AT][4], xs[AT][4];
+            if constexpr (!UP) request(0);         // (an item has a step; rows of values hold whole stages)
+            struct Sums {           // of one half of the columns: products with hi and mid, and with lo
+                int d[2][AT][4], lo[2][4];
+            };
+            struct Unit {           // sum of the values, step
+                int X[AT];
+                uint32_t step[AT];
+            };
             // The sums start at the bits of 1.5 * 2^23: an integer of at most 22 bits added to them is, read
             // as a float, that much more (128 * 255 * 128 < 2^22), so no conversion is needed.
             constexpr int BIAS = 0x4B400000;
-            auto sum_value = [](int hi, int lo) {
-                const float2 v =
-                    unpack2(add2(pack2(__int_as_float(hi), __int_as_float(lo)), pack2(-12582912.0f, -12582912.0f)));
-                return fmaf(256.0f, v.x, v.y);
+            auto value2 = [](int a, int b) {
+                return unpack2(add2(pack2(__int_as_float(a), __int_as_float(b)), pack2(-12582912.0f, -12582912.0f)));
             };
-            auto clear = [&]() {
-#pragma unroll
-                for (int n = 0; n < AT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        xs[n][k] = BIAS;
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) d[hf][0][n][k] = d[hf][1][n][k] = BIAS;
-                    }
-            };
-            // step i of the warp's range, at step j of the stage
-            // (st: the stage, xi: this lane's x values in it; plain loads, whose constant offsets fold)
-            // first: a new sum, from BIAS
-            auto mult = [&](bool first, const uint8_t* st, const uint8_t* const (&xi)[AT], int j) {
-                uint2 b[AT];
-#pragma unroll
-                for (int n = 0; n < AT; ++n) b[n] = UP ? *reinterpret_cast<const uint2*>(xi[n] + 32 * j) : bx[j][n];
-                uint4 w[RL][2];
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                    for (int r = 0; r < RL; ++r) {   // rows 4 j + t (4-bit), 8 j + t and 8 j + t + 4 (8-bit)
-                        const int row8 = BITS == 4 ? j >> 1 : j, odd = BITS == 4 ? j & 1 : r;
-                        w[r][hf] = *reinterpret_cast<const uint4*>(st + off(odd, hf) + 8 * LINE * row8);
-                    }
-#pragma unroll
-                for (int n = 0; n < AT; ++n)
-                    mma_u8s8(first, xs[n], 0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u, b[n], BIAS);
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t a[2][4];   // k 0-15 and 16-31 of the lane's four columns
-                    const uint32_t v0[4] = {w[0][hf].x, w[0][hf].y, w[0][hf].z, w[0][hf].w};
-                    if constexpr (BITS == 4) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            a[0][c] = v0[c] & 0x0F0F0F0Fu;
-                            a[1][c] = (v0[c] >> 4) & 0x0F0F0F0Fu;
-                        }
-                    } else {
-                        const uint32_t v1[4] = {w[RL - 1][hf].x, w[RL - 1][hf].y, w[RL - 1][hf].z, w[RL - 1][hf].w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            a[0][c] = v0[c];
-                            a[1][c] = v1[c];
-                        }
-                    }
-#pragma unroll
-                    for (int T = 0; T < 2; ++T)
-#pragma unroll
-                        for (int n = 0; n < AT; ++n)
-                            mma_u8s8(first, d[hf][T][n], a[0][2 * T], a[0][2 * T + 1], a[1][2 * T], a[1][2 * T + 1], b[n],
-                                        BIAS);
-                }
-            };
-            // the block (or the group) ends: acc += s step (D - z X)
-            // (k: the block's place in the stage; sz: the group's s row in it)
-            auto fold = [&](int i, int k, uint32_t sz) {
-                uint64_t step[AT], X[AT];   // twice each; X negated
+            auto read_unit = [&](int i, int j) {   // step j of the stage, i of the range
+                Unit un;
 #pragma unroll
                 for (int n = 0; n < AT; ++n) {
-                    const float st = UP ? __uint_as_float(lds32_u32(sp[n] + 4u * (i / XBLK))) : step_next[k][n];
-                    const float x = -sum_value(xs[n][0], xs[n][1]);
-                    step[n] = pack2(st, st);
-                    X[n] = pack2(x, x);
+                    uint2 w;
+                    if constexpr (UP) {
+                        w = lds64_u32(unit[n] + 8u * (i / U));
+                    } else {                       // (lanes 4 j .. 4 j + 3 have it)
+                        w.x = U == SPS ? ux[n].x : __shfl_sync(0xffffffffu, ux[n].x, 4 * j + t);
+                        w.y = U == SPS ? ux[n].y : __shfl_sync(0xffffffffu, ux[n].y, 4 * j + t);
+                    }
+                    un.X[n] = (int)w.x;
+                    un.step[n] = w.y;
+                }
+                return un;
+            };
+            // step j of the stage with one half of the columns
+            // (st: the stage; plain loads, whose constant offsets fold).  first: a new sum, from BIAS
+            auto mult = [&](Sums& m, bool first, int hf, const uint8_t* st, int j) {
+                uint4 w[RL];
+#pragma unroll
+                for (int r = 0; r < RL; ++r) {   // rows 4 j + t (4-bit), 8 j + t and 8 j + t + 4 (8-bit)
+                    const int row8 = BITS == 4 ? j >> 1 : j, odd = BITS == 4 ? j & 1 : r;
+                    w[r] = *reinterpret_cast<const uint4*>(st + off(odd, hf) + 8 * LINE * row8);
+                }
+                uint32_t a[2][4];   // k 0-15 and 16-31 of the lane's four columns
+                const uint32_t v0[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+                if constexpr (BITS == 4) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[0][c] = v0[c] & 0x0F0F0F0Fu;
+                        a[1][c] = (v0[c] >> 4) & 0x0F0F0F0Fu;
+                    }
+                } else {
+                    const uint32_t v1[4] = {w[RL - 1].x, w[RL - 1].y, w[RL - 1].z, w[RL - 1].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        a[0][c] = v0[c];
+                        a[1][c] = v1[c];
+                    }
                 }
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint2 sv = lds64_u32(sz + 64u * hf), zv = lds64_u32(sz + 64u * hf + sz_bytes / 2);
+                for (int T = 0; T < 2; ++T) {
 #pragma unroll
-                    for (int T = 0; T < 2; ++T) {   // columns 2 T and 2 T + 1
-                        const float2 sf = T16::pair(T ? sv.y : sv.x), zf = T16::pair(T ? zv.y : zv.x);
-                        const uint64_t s2 = pack2(sf.x, sf.y), z2 = pack2(zf.x, zf.y);
+                    for (int n = 0; n < AT; ++n)
+                        mma_u8s8(first, m.d[T][n], a[0][2 * T], a[0][2 * T + 1], a[1][2 * T], a[1][2 * T + 1], bx[j][n],
+                                 BIAS);
+                    mma_u8s8(first, m.lo[T], a[0][2 * T], a[0][2 * T + 1], a[1][2 * T], a[1][2 * T + 1], bx[j][AT],
+                             BIAS);
+                }
+            };
+            // the unit ends: acc += s step (D - z X), D = 256 (256 D_hi + D_mid) + D_lo
+            // (sz: the group's s row)
+            auto fold = [&](const Sums& m, const Unit& un, int hf, uint32_t sz) {
+                uint64_t st[AT], x[AT];   // twice each; X negated
 #pragma unroll
-                        for (int n = 0; n < AT; ++n) {
-                            const int(&v)[4] = d[hf][T][n];
-                            const uint64_t D = pack2(sum_value(v[0], v[1]), sum_value(v[2], v[3]));
-                            // (s step first: the other product can pass fp32's range where the result does not)
-                            acc[hf][T][n] = fma2(mul2(s2, step[n]), fma2(z2, X[n], D), acc[hf][T][n]);
-                        }
+                for (int n = 0; n < AT; ++n) {
+                    const float f = __uint_as_float(un.step[n]), v = -(float)un.X[n];
+                    st[n] = pack2(f, f);
+                    x[n] = pack2(v, v);
+                }
+                const uint2 sv = lds64_u32(sz), zv = lds64_u32(sz + sz_bytes / 2);
+#pragma unroll
+                for (int T = 0; T < 2; ++T) {   // columns 2 T and 2 T + 1
+                    const float2 sf = T16::pair(T ? sv.y : sv.x), zf = T16::pair(T ? zv.y : zv.x);
+                    const uint64_t s2 = pack2(sf.x, sf.y), z2 = pack2(zf.x, zf.y);
+                    const float2 l0 = value2(m.lo[T][0], m.lo[T][1]), l1 = value2(m.lo[T][2], m.lo[T][3]);
+#pragma unroll
+                    for (int n = 0; n < AT; ++n) {
+                        const int(&v)[4] = m.d[T][n];
+                        const float2 h0 = value2(v[0], v[1]), h1 = value2(v[2], v[3]);
+                        const uint64_t D = pack2(fmaf(256.0f, fmaf(256.0f, h0.x, h0.y), n ? l0.y : l0.x),
+                                                 fmaf(256.0f, fmaf(256.0f, h1.x, h1.y), n ? l1.y : l1.x));
+                        // (s step first: the other product can pass fp32's range where the result does not)
+                        acc[hf][T][n] = fma2(mul2(s2, st[n]), fma2(z2, x[n], D), acc[hf][T][n]);
                     }
                 }
             };
-            int gleft = p.spg - q0 % p.spg;   // steps left in the current group
-            bool fresh = false;               // the next step starts a group
-#pragma unroll 1
-            for (int i = 0; i < nq; i += SPS) {
+            // the halves h0 .. h1 - 1 of the stage from step i, unit by unit
+            auto stage = [&](int h0, int h1, int i, int gleft) {
+                const uint8_t* const st = smem + (warp * NST + slot) * STAGE;
+                uint32_t sz = sz_ring + slot * sz_bytes + 8u * cg;   // the stage's first group
+#pragma unroll
+                for (int j0 = 0; j0 < SPS; j0 += U) {
+                    if (j0 > 0 && i + j0 >= nq) break;
+                    const Unit un = read_unit(i + j0, j0);
+#pragma unroll
+                    for (int hf = h0; hf < h1; ++hf) {
+                        Sums m;
+#pragma unroll
+                        for (int j = 0; j < U; ++j) mult(m, j == 0, hf, st, j0 + j);
+                        fold(m, un, hf, sz + (BITS == 4 ? 64u * hf : 0u));
+                    }
+                    if (U < SPS && (gleft -= U) == 0) {
+                        gleft = p.spg;
+                        sz += BITS == 4 ? 128u : 64u;
+                    }
+                }
+            };
+            auto wait = [&]() {
                 if (ok) {
                     const bool good = mbar_wait_bounded(&bar[slot], phase, WAIT_NS);
                     if (!good) atomicOr(&g_moe_status, 1u);
                     ok = __all_sync(0xffffffffu, good);
                 }
-                if (!ok) break;
-                const uint8_t* const st = smem + (warp * NST + slot) * STAGE;
-                uint32_t sz = sz_ring + slot * sz_bytes + 8u * cg;   // the stage's first group
-                const uint8_t* xi[AT];
-#pragma unroll
-                for (int n = 0; n < AT; ++n) xi[n] = UP ? smem + xa[n] + 32u * i : nullptr;
-                // D starts anew with each fixed-point block (xb steps from the start of the range) and each group
-                if (i + SPS <= nq && gleft >= SPS && SPS <= xb) {   // a whole stage inside one group and block
-                    if constexpr (SPS == XBLK) {
-                        mult(true, st, xi, 0);
-                    } else {
-                        if (i % xb == 0 || fresh) clear();
-                        mult(false, st, xi, 0);
-                    }
-                    fresh = false;
-#pragma unroll
-                    for (int j = 1; j < SPS; ++j) mult(false, st, xi, j);
-                    gleft -= SPS;
-                    if (SPS == XBLK || (i + SPS) % xb == 0 || gleft == 0 || i + SPS >= nq) fold(i, 0, sz);
-                    if (gleft == 0) {
-                        gleft = p.spg;
-                        fresh = true;
-                    }
-                } else {                               // short groups, or the range's end: step by step
-#pragma unroll
-                    for (int j = 0; j < SPS; ++j) {
-                        if (i + j >= nq) break;
-                        if ((i + j) % xb == 0 || fresh) clear();
-                        fresh = false;
-                        mult(false, st, xi, j);
-                        if (--gleft == 0 || (i + j + 1) % xb == 0 || i + j + 1 == nq)
-                            fold(i + j, SPS == 4 && xb == 2 ? j / 2 : 0, sz);
-                        if (gleft == 0) {
-                            gleft = p.spg;
-                            fresh = true;
-                            sz += 128u;
-                        }
-                    }
-                }
-                if constexpr (!UP) request(i + SPS);
-                __syncwarp();   // every lane has read the stage: refill it
+                return ok;
+            };
+            auto release = [&]() {   // every lane has read the stage: refill it
+                __syncwarp();
                 fence_proxy_async_smem();
                 issue(slot);
                 advance();
+            };
+            int gleft = p.spg - q0 % p.spg;   // steps left in the current group
+#pragma unroll 1
+            for (int i = 0; i < nq; i += SPS) {
+                if constexpr (UP) request(i);
+                if (!wait()) break;
+                if constexpr (BITS == 4) {
+                    stage(0, 2, i, gleft);
+                } else {
+                    stage(0, 1, i, gleft);
+                    release();
+                    if (!wait()) break;
+                    stage(1, 2, i, gleft);
+                }
+                if (!UP && i + SPS < nq) request(i + SPS);
+                release();
+                if constexpr (U < SPS) {
+                    gleft -= SPS;
+                    while (gleft <= 0) gleft += p.spg;
+                }
             }
             if constexpr (!UP) {
                 if (p.rows != nullptr) {   // the rows of this (warp, block), to be summed at the end
@@ -905,26 +958,39 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
 #pragma unroll
                 for (int d = LPS / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const uint32_t E = block_exponent(top);
-                uint2 hi, lo;
-                to_fixed<8>(v, __uint_as_float((268u - E) << 23), hi, lo);   // bytes 0 1 2 3 in .x
+                const Bytes b = to_fixed<8>(v, block_inverse(E));   // bytes 0 1 2 3 in .x
+                int sum = value_sum(b);                             // of 8 lanes, a step, and of its unit (8, 16 or 32)
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1)
+                    if (d < 8 << p.hlog) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 const int slot = slots[pos], q = cc / SK;
-                int8_t* const row = p.hq + ((size_t)(2 * slot) * p.Qh + q) * SK;   // lo: Qh * SK bytes on
+                const size_t plane = (size_t)p.Qh * SK;
+                int8_t* const row = p.hq + ((size_t)(3 * slot) * p.Qh + q) * SK;   // hi, then mid and lo, a plane each
                 const bool in = mine && q < p.Qh && check(slot >= 0 && slot < p.S, &g_moe_status);
                 if constexpr (BITS == 4) {
-                    // a word row's 8 values are two lanes': the even one stores hi, the odd one lo, as 0 2 4 6 1 3 5 7
+                    // a word row's 8 values are two lanes': the even one stores hi and lo, the odd one mid, as 0 2 4 6
+                    // 1 3 5 7
                     const bool odd = lane & 1;
-                    const uint32_t give = odd ? hi.x : lo.x, keep = odd ? lo.x : hi.x;
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 1);
-                    const uint32_t a = odd ? got : keep, b = odd ? keep : got;   // values 0-3 and 4-7
-                    if (in)
-                        *reinterpret_cast<uint2*>(row + (odd ? (size_t)p.Qh * SK : 0) + 8 * (c % SK / 8)) =
-                            make_uint2(prmt(a, b, 0x6420u), prmt(a, b, 0x7531u));
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? b.hi.x : b.mid.x, 1);
+                    const uint32_t lo2 = __shfl_xor_sync(0xffffffffu, b.lo.x, 1);
+                    const uint32_t u0 = odd ? got : b.hi.x, u1 = odd ? b.mid.x : got;   // values 0-3 and 4-7
+                    int8_t* const to = row + 8 * (c % SK / 8);
+                    if (in) {
+                        *reinterpret_cast<uint2*>(to + (odd ? plane : 0)) =
+                            make_uint2(prmt(u0, u1, 0x6420u), prmt(u0, u1, 0x7531u));
+                        if (!odd)
+                            *reinterpret_cast<uint2*>(to + 2 * plane) =
+                                make_uint2(prmt(b.lo.x, lo2, 0x6420u), prmt(b.lo.x, lo2, 0x7531u));
+                    }
                 } else if (in) {   // word row j of the step: bytes 8 (j % 4) + 4 (j / 4)
                     const int j = c % SK / 4, o = 8 * (j & 3) + 4 * (j >> 2);
-                    *reinterpret_cast<uint32_t*>(row + o) = hi.x;
-                    *reinterpret_cast<uint32_t*>(row + (size_t)p.Qh * SK + o) = lo.x;
+                    *reinterpret_cast<uint32_t*>(row + o) = b.hi.x;
+                    *reinterpret_cast<uint32_t*>(row + plane + o) = b.mid.x;
+                    *reinterpret_cast<uint32_t*>(row + 2 * plane + o) = b.lo.x;
                 }
-                if (in && lane % LPS == 0) p.hstep[(size_t)slot * p.Qh + q / (TC / 2 / SK)] = block_step(top, E);
+                if (in && (lane & ((8 << p.hlog) - 1)) == 0)
+                    p.hunit[(size_t)((slot * p.Qh + q) >> p.hlog)] =
+                        make_uint2((uint32_t)sum, block_step(top, E));
             }
             ++done;
             __syncwarp();
@@ -1039,35 +1105,40 @@ moe_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUten
     }
 }
 
-// Dynamic shared memory a CTA of 12 or 16 warps (one per SM), or of 6 or 8 (two), can have.
-constexpr int max_smem(int W) { return W > 8 ? 225 * 1024 : 112 * 1024; }
-constexpr int ring_bytes(int W, int sz_rows) { return 1024 + W * NST * (STAGE + 256 * sz_rows); }
+// Dynamic shared memory a CTA of 12 or 16 warps (one per SM), or of 6 or 8 (two), can have.  (227 KB, less 320 bytes for
+// the static part.)
+constexpr int WHOLE_SM = 227 * 1024 - 320;
+constexpr int max_smem(int W) { return W > 8 ? WHOLE_SM : 112 * 1024; }
+constexpr int ring_bytes(int W, int bits, int sz_rows) { return 1024 + W * NST * (STAGE + sz_space(bits, sz_rows)); }
 // s rows of the groups that a stage of `sps` steps, starting at a multiple of them, can touch.
 int stage_groups(int spg, int sps) { return spg % sps == 0 ? 1 : std::min(sps, (sps - 1) / spg + 2); }
 
 int xcol_bytes(int steps) {   // 32 mod 128: the four columns of a load phase lie in different banks
-    const int b = steps * 32;
+    const int b = (steps + XBLK - 1) / XBLK * XBLK * 32;
     return b + (160 - b % 128) % 128;
 }
 // How a product of inner length K is cut.
 struct Cut {
-    int spg, sz_rows;     // steps per group, s rows per stage
+    int bits, spg, sz_rows;   // steps per group, s rows per stage
     int bt;               // slots per block
     int W, cluster;       // warps; CTAs per column tile (DOWN)
     bool rows;            // DOWN: rows in global memory instead of the warps' own sums
-    int xcol, nsteps, smem;
+    int xcol, nunits, nblk, smem;
+    int ulog;             // steps per unit, log2: the most, up to a fixed-point block, that no group ends inside
 };
+int unit_log(int spg) { return spg % 4 == 0 ? 2 : spg % 2 == 0 ? 1 : 0; }
 
 // DOWN with rows: the most that a CTA stages at a time, its tokens' slots.
 int staged_rows(int T, int top_k, int cluster) {
     return std::min(tokens_at_once(top_k), (T + cluster - 1) / cluster) * top_k;
 }
 
-void cut_smem(Cut& c, bool up, int T, int S, int Q) {
+void cut_smem(Cut& c, bool up, int T, int S, int E, int Q) {
     c.xcol = up ? xcol_bytes(Q) : 0;
-    c.nsteps = up ? (Q + XBLK - 1) / XBLK : 0;
-    c.smem = ring_bytes(c.W, c.sz_rows) + (up ? steps_at(c.W, c.bt, S, c.xcol) + c.bt * c.nsteps * 4
-                                              : values_at(0, c.bt, S) + (c.rows ? 0 : c.W * T * MCOLS * 4));
+    c.nunits = up ? (Q + (1 << c.ulog) - 1) >> c.ulog : 0;
+    c.nblk = most_blocks(S, E, c.bt);
+    c.smem = ring_bytes(c.W, c.bits, c.sz_rows) + (up ? units_at(c.W, c.bt, S, c.nblk, c.xcol) + c.bt * c.nunits * 8
+                                              : values_at(0, c.bt, S, c.nblk) + (c.rows ? 0 : c.W * T * MCOLS * 4));
     if (!up && c.rows) c.smem = std::max(c.smem, 1024 + PART_AT + staged_rows(T, S / T, c.cluster) * MCOLS * 4);
 }
 
@@ -1084,19 +1155,25 @@ Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
     const int Q = (K + SK - 1) / SK;
     Cut c{};
     c.spg = group_size == -1 || group_size == K ? 1 << 29 : group_size / SK;
-    c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
+    c.bits = bits;
+    c.sz_rows = stage_groups(c.spg, XBLK);
+    c.ulog = unit_log(c.spg);
     c.cluster = 1;
     if (T <= 4 && (long long)((I + 63) / 64) * std::min(S, E) <= sm_count()) {
         c.W = 8;
-        c.bt = 4;
-        cut_smem(c, true, T, S, Q);
+        c.bt = T;
+        cut_smem(c, true, T, S, E, Q);
         if (c.smem <= max_smem(8)) return c;
     }
     c.W = up_warps(T <= 4 ? 1 : 2);
-    for (c.bt = T <= 4 ? 4 : MAXBT; c.bt > 0; --c.bt) {
-        cut_smem(c, true, T, S, Q);
-        if (c.smem <= max_smem(c.W)) break;
+    for (c.bt = std::min(T, MAXBT); c.bt > 0; --c.bt) {
+        cut_smem(c, true, T, S, E, Q);
+        if (c.smem <= max_smem(c.W)) return c;
     }
+    c.W = T <= 4 ? 8 : c.W;   // (T <= 4, K above 20000, short groups: 8 warps, one CTA per SM)
+    c.bt = 1;
+    cut_smem(c, true, T, S, E, Q);
+    if (c.smem > WHOLE_SM) c.bt = 0;
     return c;
 }
 
@@ -1110,7 +1187,7 @@ int clusters_that_fit(int cs) {
     if (n > 0) return n;
     n = 2 * sm_count() / cs;
     if (cs > 1) {
-        auto kern = moe_kernel<4, false, 1, false, down_warps(1)>;
+        auto kern = moe_kernel<4, false, 1, false, down_warps(1), XBLK>;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(cs, 1, 1);
         cfg.blockDim = dim3(down_warps(1) * 32, 1, 1);
@@ -1133,22 +1210,24 @@ int clusters_that_fit(int cs) {
 }
 
 // DOWN with clusters of a given size.
-Cut cut_down(int T, int S, int I, int group_size, int bits, int cluster) {
+Cut cut_down(int T, int S, int E, int I, int group_size, int bits, int cluster) {
     Cut c{};
     c.W = down_warps(T <= 4 ? 1 : 2);
     c.spg = group_size == -1 || group_size == I ? 1 << 29 : group_size / SK;
-    c.sz_rows = stage_groups(c.spg, bits == 4 ? 4 : 2);
+    c.bits = bits;
+    c.sz_rows = stage_groups(c.spg, XBLK);
     c.bt = T <= 4 ? 4 : MAXBT;
+    c.ulog = unit_log(c.spg);
     c.cluster = cluster;
     c.rows = T > SUMS_T;
-    cut_smem(c, false, T, S, 0);   // (at most 92 KB)
+    cut_smem(c, false, T, S, E, 0);   // (at most 92 KB)
     return c;
 }
 
 // DOWN: a column tile is worked on by a cluster, of the size that leaves the fewest places of the SMs without a CTA:
 // two per SM, or one when there is little to do and UP still holds the other.  (A sixteenth of the clusters that fit
 // an empty device is kept back: 32 clusters of 8 where 33 fit ran in two waves behind UP.)
-Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
+Cut cut_down(int T, int S, int E, int I, int N, int group_size, int bits, bool few) {
     const int places = few ? sm_count() : 2 * sm_count();
     const int tiles = (N + MCOLS - 1) / MCOLS;
     int best = -1, cluster = 1;   // places taken, in percent
@@ -1161,20 +1240,18 @@ Cut cut_down(int T, int S, int I, int N, int group_size, int bits, bool few) {
             cluster = cs;
         }
     }
-    return cut_down(T, S, I, group_size, bits, cluster);
+    return cut_down(T, S, E, I, group_size, bits, cluster);
 }
 
-template <int BITS, bool BF, int NT, bool UP, int W>
-wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, bool pdl, cudaStream_t stream) {
-    auto kern = moe_kernel<BITS, BF, NT, UP, W>;
+template <int BITS, bool BF, int NT, bool UP, int W, int U>
+wq_status launch_kernel(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, bool pdl, cudaStream_t stream) {
+    auto kern = moe_kernel<BITS, BF, NT, UP, W, U>;
     static std::atomic<uint64_t> attr_ctx[MAX_DEVICES];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
-    if (const wq_status st = ensure_smem_attr((const void*)kern, max_smem(W), attr_ctx, dev); st != WQ_OK) return st;
-    // More blocks than these cannot be: each expert's last block may be short.
-    const int blocks = std::min(p.S, std::min(p.E, p.S) + p.S / p.bt);
+    if (const wq_status st = ensure_smem_attr((const void*)kern, UP ? WHOLE_SM : max_smem(W), attr_ctx, dev); st != WQ_OK) return st;
     cudaLaunchConfig_t cfg{};
-    const long long ctas = UP ? std::min<long long>(sm_count() * (16 / W), (long long)blocks * p.ntiles)
+    const long long ctas = UP ? std::min<long long>(sm_count() * (16 / W), (long long)p.nblk * p.ntiles)
                               : (long long)p.ntiles * p.cluster;
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(W * 32, 1, 1);
@@ -1199,6 +1276,15 @@ wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, int smem, b
     return from_cuda(cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], p));
 }
 
+template <int BITS, bool BF, int NT, bool UP, int W>
+wq_status launch_one(const CUtensorMap (&tm)[3], const MoeParams& p, const Cut& c, bool pdl, cudaStream_t stream) {
+    switch (UP ? c.ulog : p.hlog) {
+        case 2: return launch_kernel<BITS, BF, NT, UP, W, 4>(tm, p, c.smem, pdl, stream);
+        case 1: return launch_kernel<BITS, BF, NT, UP, W, 2>(tm, p, c.smem, pdl, stream);
+        default: return launch_kernel<BITS, BF, NT, UP, W, 1>(tm, p, c.smem, pdl, stream);
+    }
+}
+
 // One product: its shape, its launch.
 template <int BITS, bool BF, bool UP>
 wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const uint16_t* z, int K, int group_size,
@@ -1207,15 +1293,16 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
     p.Kw = K * BITS / 32;
     p.Q = (K + SK - 1) / SK;
     p.bt = c.bt; p.spg = c.spg; p.sz_rows = c.sz_rows;
-    p.cluster = c.cluster; p.xcol = c.xcol; p.nsteps = c.nsteps;
+    p.cluster = c.cluster; p.xcol = c.xcol; p.nunits = c.nunits; p.nblk = c.nblk;
     p.groups = group_size == -1 ? 1 : K / group_size;
-    // UP: planes of I columns, gate and up; DOWN: rows of N columns (words in boxes of 32, s and z of 64)
+    // UP: planes of I columns, gate and up; DOWN: rows of N columns (words in boxes of 32; 4-bit: s and z of both halves)
     CUtensorMap tm[3];
     const uint64_t cols = UP ? p.I : p.NW, planes = UP ? 2 : 1, wrows = (uint64_t)p.E * p.Kw;
     const uint64_t srows = (uint64_t)p.E * p.groups;
-    const uint32_t sc = UP ? 32 : 64, bp = UP ? 2 : 1;
+    const uint32_t sc = UP || BITS == 8 ? 32 : 64, bp = UP && BITS == 4 ? 2 : 1;
     const int dims = UP ? 3 : 2;
-    if (!make_map_rows(&tm[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, w, 4, dims, cols, planes, wrows, 32, bp, BOX_ROWS,
+    if (!make_map_rows(&tm[0], CU_TENSOR_MAP_DATA_TYPE_UINT32, w, 4, dims, cols, planes, wrows, 32, bp,
+                       stage_rows<BITS>(),
                        CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_rows(&tm[1], CU_TENSOR_MAP_DATA_TYPE_UINT16, s, 2, dims, cols, planes, srows, sc, bp, p.sz_rows,
                        CU_TENSOR_MAP_SWIZZLE_NONE) ||
@@ -1225,19 +1312,20 @@ wq_status run_product(MoeParams& p, const uint32_t* w, const uint16_t* s, const 
     const int tc = UP ? MCOLS / 2 * (c.W / along_k(c.W)) : MCOLS;   // columns of h or y per tile
     p.ntiles = ((UP ? p.I : p.NW) + tc - 1) / tc;
     if constexpr (UP) {
-        if (c.W == 8) return launch_one<BITS, BF, 1, UP, 8>(tm, p, c.smem, pdl, stream);
-        return c.W == up_warps(1) ? launch_one<BITS, BF, 1, UP, up_warps(1)>(tm, p, c.smem, pdl, stream)
-                         : launch_one<BITS, BF, 2, UP, up_warps(2)>(tm, p, c.smem, pdl, stream);
+        if (c.W == 8) return launch_one<BITS, BF, 1, UP, 8>(tm, p, c, pdl, stream);
+        return c.W == up_warps(1) ? launch_one<BITS, BF, 1, UP, up_warps(1)>(tm, p, c, pdl, stream)
+                         : launch_one<BITS, BF, 2, UP, up_warps(2)>(tm, p, c, pdl, stream);
     } else {
-        return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, down_warps(1)>(tm, p, c.smem, pdl, stream)
-                         : launch_one<BITS, BF, 2, UP, down_warps(2)>(tm, p, c.smem, pdl, stream);
+        return c.bt <= 4 ? launch_one<BITS, BF, 1, UP, down_warps(1)>(tm, p, c, pdl, stream)
+                         : launch_one<BITS, BF, 2, UP, down_warps(2)>(tm, p, c, pdl, stream);
     }
 }
 
-// Workspace: h's two bytes per value, then its steps (at most one per step of K); then DOWN's rows.
+// Workspace: h's three bytes per value, then its units (at most one per step of K); then DOWN's rows.
+int h_steps(int I) { return (I + SK * XBLK - 1) / (SK * XBLK) * XBLK; }   // whole stages
 size_t h_bytes(int S, int I) {
-    const size_t rows = (size_t)S * ((I + SK - 1) / SK);
-    return (rows * (2 * SK + 4) + 255) & ~(size_t)255;
+    const size_t rows = (size_t)S * h_steps(I);
+    return (rows * (3 * SK + 8) + 255) & ~(size_t)255;
 }
 
 template <int BITS, bool BF>
@@ -1256,18 +1344,19 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
         last.group_size != m.group_size || last.sms != sms) {
         last = Plan{p.T, p.S, p.E, m.K, m.I, m.N, m.group_size, sms, {}, {}};
         last.up = cut_up(m.T, p.S, p.E, m.K, m.I, m.group_size, BITS);
-        last.down = cut_down(m.T, p.S, m.I, m.N, m.group_size, BITS, last.up.W == 8);
+        last.down = cut_down(m.T, p.S, m.E, m.I, m.N, m.group_size, BITS, last.up.W == 8);
     }
     const Cut up = last.up, down = last.down;
-    p.Qh = (m.I + SK - 1) / SK;
-    p.hb = MCOLS * (up.W / along_k(up.W)) / 2 / SK;   // a tile of UP: 128 values or 64
+    p.Qh = h_steps(m.I);
+    const int hb = MCOLS * (up.W / along_k(up.W)) / 2 / SK;   // a tile of UP, steps of h: 4, or 2
+    p.hlog = std::min(down.ulog, hb / 2);                     // (4 steps: 2, 2 steps: 1)
     // (before anything is launched: what must fit 31 bits -- the weighted line of work, word rows, CTAs)
     const long long units = std::max((m.I + 31) / 32, (p.Qh + XBLK - 1) / XBLK), most = 1ll << 31;
     if (up.bt == 0 || down.bt == 0 || p.S * 5 * units >= most || (long long)p.E * (m.K * BITS / 32) >= most ||
         (long long)p.E * ((long long)m.I * BITS / 32) >= most || (m.N + 63ll) / 64 * 8 >= most)
         return WQ_ERR_UNSUPPORTED;
     p.hq = static_cast<int8_t*>(m.ws);
-    p.hstep = reinterpret_cast<float*>(p.hq + (size_t)2 * p.S * p.Qh * SK);
+    p.hunit = reinterpret_cast<uint2*>(p.hq + (size_t)3 * p.S * p.Qh * SK);
     if (down.rows) p.rows = reinterpret_cast<float*>(static_cast<uint8_t*>(m.ws) + h_bytes(p.S, m.I));
     p.NW = 2 * m.I;
     const wq_status st = run_product<BITS, BF, true>(p, m.w_up, m.s_up, m.z_up, m.K, m.group_size, up,
@@ -1287,8 +1376,8 @@ size_t moe_workspace_bytes(int T, int top_k, int I, int N) {
 // What DOWN asks for with clusters of the given size, and the end of what it touches (the round-up of the rings to 1024
 // bytes among it).
 size_t moe_down_smem(int T, int top_k, int I, int bits, int group_size, int cluster, size_t* used) {
-    const Cut c = cut_down(T, T * top_k, I, group_size, bits, cluster);
-    const int tables = ring_bytes(c.W, c.sz_rows) - 1 + values_at(0, c.bt, T * top_k);
+    const Cut c = cut_down(T, T * top_k, WQ_MOE_MAX_EXPERTS, I, group_size, bits, cluster);
+    const int tables = ring_bytes(c.W, bits, c.sz_rows) - 1 + values_at(0, c.bt, T * top_k, c.nblk);
     *used = c.rows ? std::max(tables, 1023 + PART_AT + staged_rows(T, top_k, cluster) * MCOLS * 4)
                    : tables + c.W * T * MCOLS * 4;
     return c.smem;

@@ -402,7 +402,7 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  *   h[t][j] = act(x[t] @ Wg[e]) * (x[t] @ Wu[e]),  e = ids[t][j]
  *   y[t]    = sum_j weights[t][j] * (h[t][j] @ Wd[e])
  * in two launches; a chosen expert's words are read once for every 8 slots that it
- * has (fewer with a K above 5000).
+ * has (fewer with a K above 4000).
  *   x        (T, K), y (T, N): binary16, or bfloat16 with WQ_FLAG_BF16, as all s and z.
  *   ids      (T, top_k) int32, weights (T, top_k) fp32: as wq_moe_route writes
  *            them.  An id outside 0 .. E-1 leaves its slot empty; a token whose
@@ -414,12 +414,13 @@ wq_status wq_moe_route(const void* logits, int type, int T, int E, int64_t ld, i
  *   activation  WQ_ACT_SILU: g / (1 + exp(-g)); WQ_ACT_GELU: g * Phi(g), the exact form.
  *   workspace   wq_moe_workspace_size() bytes of device memory, 256-byte aligned,
  *            any contents; calls that may run at the same time must not share it.
- * The codes are multiplied as integers: x and h become 16-bit fixed
+ * The codes are multiplied as integers: x and h become 24-bit fixed
  * point, with a power-of-two step per token and aligned block of at most 128 values
- * that puts the block's largest between 2^14 and 2^15 (error at most 2^-15 of
- * that value; none for values that end at or above the step).  Their products
- * are summed exactly over a block, blocks and slots in fp32, in an order that
- * does not depend on timing; y is rounded once.  A row of x that holds NaN or an
+ * that puts the block's largest between 2^22 and 2^23: as near as fp32 sums with a
+ * value of that size come (error at most 1.02 * 2^-23 of it; none for values that end
+ * at or above the step, a bf16 within 2^-15 of the largest, an fp16 within 2^-12).
+ * Their products are summed exactly over a block, blocks and slots in fp32, in an
+ * order that does not depend on timing; y is rounded once.  A row of x that holds NaN or an
  * infinity becomes NaN; no other row does.
  * bits 4 or 8 (else WQ_ERR_UNSUPPORTED).  1 <= T <= WQ_MOE_MAX_TOKENS,
  * 1 <= top_k <= 16, 1 <= E <= WQ_MOE_MAX_EXPERTS, K <= WQ_MOE_MAX_K.  K and
