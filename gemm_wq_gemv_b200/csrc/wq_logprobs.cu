@@ -11,7 +11,8 @@
 // to 8 CTAs splits it and joins through distributed shared memory.
 //  * Each thread keeps its own reference m, S1 and S2 and moves m only when a
 //    vector's maximum exceeds it by 8: e^8 times the count stays far inside
-//    fp32, and the rescaling branch becomes rare.
+//    fp32, and the rescaling branch becomes rare.  After 1024 terms the sums go
+//    to a total, so that a row's length does not cost digits.
 //  * Top entries without a second pass.  A thread also keeps the largest value
 //    it met and the first vector that held it.  The k-th largest of these
 //    (value, vector) pairs over the CTA is a floor: k elements are at or above
@@ -42,6 +43,10 @@ constexpr int LT = 256;        // threads per CTA
 constexpr int LW = LT / 32;
 constexpr int CAP = 1024;      // entries at or above the floor that are ranked at once
 constexpr int MAXK = 32;
+// Steps of the main loop (4 vectors: 32 or 16 terms) that a thread adds into one sum; then it goes to the thread's total
+// in shared memory, so that a sum's error does not grow with the row: at most 1024 + V / 2^18 additions in a chain.  (One
+// chain of a row of 2^29 was off by 1e-3.)
+constexpr int CHAIN = 32;
 constexpr float LOWEST = -1000.0f;  // e^-1000 = 0 in fp32: stands in for l - M = -inf, whose product with 0 is NaN
 
 struct LpParams {
@@ -212,15 +217,38 @@ __global__ void __launch_bounds__(LT, 5) logprobs_kernel(const LpParams p) {
         v += LT;
     }
     const int vend = min(v1, full1);
-    for (; v + (U - 1) * LT < vend; v += U * LT) {
-        uint4 r[U];
+    Sums* const total = reinterpret_cast<Sums*>(sh.cand) + tid;   // this thread's, where its row is long
+    auto join = [&]() {   // s and the total
+        Sums t = *total;
+        const float M = fmaxf(s.m, t.m);
+        rebase(s, M);
+        rebase(t, M);
+        s.s1 += t.s1;
+        s.s2 += t.s2;
+    };
+    const int last = vend - (U - 1) * LT;   // a step begins below it
+    int stop = min(last, v + CHAIN * U * LT);
+    bool lengthy = false;
+    while (true) {
+        for (; v < stop; v += U * LT) {
+            uint4 r[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) r[j] = __ldg(vecs + v + j * LT);
+            for (int j = 0; j < U; ++j) r[j] = __ldg(vecs + v + j * LT);
 #pragma unroll
-        for (int j = 0; j < U; ++j) vector(v + j * LT, r[j]);
+            for (int j = 0; j < U; ++j) vector(v + j * LT, r[j]);
+        }
+        if (v >= last) break;
+        // into the total, and a new chain with the same reference
+        const float m = s.m;
+        if (lengthy) join();
+        *total = s;
+        s = Sums{m, 0.0f, 0.0f};
+        lengthy = true;
+        stop = min(last, v + CHAIN * U * LT);
     }
     for (; v < vend; v += LT) vector(v, __ldg(vecs + v));
     if (v < v1) partial(v);
+    if (lengthy) join();
 
     // ---- the CTA's sums
     {
