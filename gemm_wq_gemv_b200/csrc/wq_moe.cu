@@ -1333,16 +1333,18 @@ wq_status run_moe(const MoeProblem& m, cudaStream_t stream) {
     MoeParams p{};
     p.x = m.x; p.ids = m.ids; p.weights = m.weights; p.y = m.y;
     p.T = m.T; p.top_k = m.top_k; p.S = m.T * m.top_k; p.E = m.E; p.I = m.I; p.act = m.act;
-    // the cuts of this thread's last shape: a decode loop asks for the same ones again
+    // the cuts of this thread's last shape: a decode loop asks for the same ones again (per device: two with the same SMs
+    // may hold different numbers of clusters)
     struct Plan {
-        int T, S, E, K, I, N, group_size, sms;
+        int T, S, E, K, I, N, group_size, dev;
         Cut up, down;
     };
     static thread_local Plan last{};
-    const int sms = sm_count();
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WQ_ERR_CUDA;
     if (last.T != p.T || last.S != p.S || last.E != p.E || last.K != m.K || last.I != m.I || last.N != m.N ||
-        last.group_size != m.group_size || last.sms != sms) {
-        last = Plan{p.T, p.S, p.E, m.K, m.I, m.N, m.group_size, sms, {}, {}};
+        last.group_size != m.group_size || last.dev != dev) {
+        last = Plan{p.T, p.S, p.E, m.K, m.I, m.N, m.group_size, dev, {}, {}};
         last.up = cut_up(m.T, p.S, p.E, m.K, m.I, m.group_size, BITS);
         last.down = cut_down(m.T, p.S, m.E, m.I, m.N, m.group_size, BITS, last.up.W == 8);
     }
