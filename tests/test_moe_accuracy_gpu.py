@@ -117,6 +117,17 @@ def test_long_rows(cuda, libwq, T, K, I, bits, G):
     moe_oracle.assert_close(run(libwq, p, bits, G, "silu", cuda), ref, tol)
 
 
+@pytest.mark.parametrize("bits,G", [(4, 32), (8, -1)])
+def test_the_longest_rows_and_the_most_slots(cuda, libwq, bits, G):
+    import torch
+    p = moe_oracle.problem(64, 16, 16, 24576, 32, 8, bits, G, torch.float16, seed=77)
+    y = run(libwq, p, bits, G, "silu", cuda)
+    on = {n: tuple(t.to(cuda) for t in v) if isinstance(v, tuple) else v.to(cuda) if isinstance(v, torch.Tensor) else v
+          for n, v in p.items()}
+    ref, tol = moe_grouped.layer(on, bits, "silu", product)
+    moe_oracle.assert_close(y, ref.cpu(), tol.cpu())
+
+
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
 @pytest.mark.parametrize("T,E,k,K,I,N,bits,G", [
     (1, 64, 8, 2048, 1024, 2048, 4, 128), (12, 8, 2, 2048, 1408, 2048, 4, 128), (40, 16, 4, 2048, 768, 2048, 8, 128),
