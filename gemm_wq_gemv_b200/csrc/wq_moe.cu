@@ -23,9 +23,9 @@
 //    copies are joined at the end, across the cluster through distributed shared memory.
 //    With more, the copies do not fit: a warp leaves the rows of its (block, part) in
 //    global memory (L2), and the cluster sums them at its end.  Both in a fixed order.
-//    (Instead of rows, 32 tokens: 85 us; a split of K over the CTA's warps with two
-//    barriers per item 95 us, one copy per CTA with the warps adding in turn 97 us; a last
-//    CTA to arrive that sums rows cost 1 us per item for the fence, up to 17 us at the end.)
+//    (On an earlier form, instead of rows, 32 tokens: 85 us; a split of K over the CTA's warps
+//    with two barriers per item 95 us, one copy per CTA with the warps adding in turn 97 us; a
+//    last CTA to arrive that sums rows cost 1 us per item for the fence, up to 17 us at the end.)
 //  * Products on integers.  Unpacking codes to fp16 or bf16 costs 7 instructions
 //    per word of 8 codes, and with m16n8k16 (2.1 clocks per SM on B200) that held
 //    a first version to 2.4 TB/s.  So the codes stay integers: 4-bit codes become
@@ -59,12 +59,12 @@
 //  * DOWN is a programmatic dependent of UP: it finds its blocks and requests its
 //    first words while UP drains, and waits only before it reads h.
 // Measured (B200, device time): 16 tokens, 2 of 8 experts of 4096 x 11008, 4-bit, 569 MB:
-// 120 us, 4.7 TB/s (UP 66 us for 383 MB, DOWN 53 us for 195 MB); 48 tokens, 4 of 32 experts
-// of 2048 x 1408, 8-bit, 285 MB: 83 us, 3.4 TB/s; 1 token, 8 of 64 experts of 2048 x 1024,
-// 4-bit, 27 MB: 14.6 us.  UP is held by its SMs' last items (12 to 20 us each; a part of the
-// line is 2 to 6 of them) and, where an expert has more than 4 tokens, by a second MMA per
-// operand and twice the folds; DOWN by the latency of its chain, a stage every 2000 cycles
-// per warp; 1 token by the two starts (blocks, first loads, the join: 9 of 14.6 us).
+// 119 us, 4.8 TB/s; 48 tokens, 4 of 32 experts of 2048 x 1408, 8-bit, 285 MB: 79 us, 3.6 TB/s;
+// 1 token, 8 of 64 experts of 2048 x 1024, 4-bit, 27 MB: 14.2 us.  With 16 tokens neither DRAM
+// (65 % of the copy rate in UP, 59 % in DOWN), the issue slots (46 and 41 %) nor the tensor pipe
+// (36 %) is full: three warps per scheduler wait for their own chains (stage, unpacking, MMAs,
+// fold), and UP's SMs end at different times (a part of the line is 2 to 6 items of 12 to
+// 20 us); 1 token is the two starts (blocks, first loads, the join: 9 of 14.2 us).
 // Every mbarrier wait is bounded; on time-out the kernel records it in its status
 // word and skips the rest of the warp's work.
 #include <cuda_bf16.h>
@@ -88,8 +88,9 @@ namespace {
 constexpr int MCOLS = 64;       // weight columns per warp (two halves of 32)
 constexpr int MAXBT = 8;        // slots per block
 // Most tokens for which every warp of DOWN keeps sums of y of its own; with more it leaves rows in global memory.  (Rows
-// against sums, 16 tokens of 64 experts: 59.7 us against 55.7; 5 tokens, small: 18.5 us against 13.7; 32 tokens, for
-// which sums would fit with groups of 64 or more only: 72.6 us against 70.0.)
+// against sums, 16 tokens of 64 experts: 58.1 us against 55.1; 5 tokens, small: 19.0 against 14.5.  32 tokens of 64
+// experts: rows 84.2, sums 80.6; of 128 experts of 7168 x 512 164 and 156: with a copy of 32 tokens the shared memory
+// fills to 2 KB.)
 constexpr int SUMS_T = 16;
 constexpr int SK = 32;          // values of K per step (one MMA)
 constexpr int XBLK = 4;         // steps per block of fixed-point values
@@ -101,11 +102,12 @@ template <int BITS> constexpr int stage_rows() { return BITS == 4 ? 16 : 32; }
 // Space for a stage's s rows and its z rows (64 or 32 columns), each at a multiple of 128 bytes.
 __host__ __device__ constexpr int sz_space(int bits, int rows) { return bits == 4 ? 256 * rows : (rows + 1) / 2 * 256; }
 constexpr int NST = 2;          // ring stages per warp (DOWN with 3: the same time)
-// Warps of a CTA with NT token tiles.  Two tiles need about 160 registers: with 16 warps per SM, and 128, the spilled
-// ones passed through L2, shared memory leaving little L1.  So 12 per SM, UP 12 in one CTA, DOWN 6 in each of two
-// (DOWN with 8: 16 tokens, 2 of 8 experts, 148 us against 121 us; 16 of 64 experts 62.5 against 55.6; 48 tokens, 8-bit,
-// 88.6 against 83.5; UP with 16: 48 tokens 90 against 88, 16 tokens 120 against 121).  One tile: 16 per SM (1 token:
-// 14.6 us; DOWN with 6 in a CTA 15.8).
+// Warps of a CTA with NT token tiles.  Two tiles need about 160 registers: with 16 warps per SM, and 128, some spill, and
+// 16 warps' rings leave fewer slots per block.  So 12 per SM, UP 12 in one CTA, DOWN 6 in each of two (DOWN with 8:
+// 16 tokens, 2 of 8 experts, 131.3 us against 128.0; 8 tokens, top 4 of 16 of 7168 x 2048, 83.1 against 81.9; its sums do
+// not fit groups of 32.  UP with 16: 16 tokens, 2 of 8, 130.9 against 128.0, 64 tokens, 2 of 8 of 4096 x 4096, 142.6
+// against 132.5, 24 tokens of 8192 x 2048 91.6 against 85.8; but 48 tokens, 8-bit, 75.9 against 78.6, 16 tokens with
+// groups of 32 44.1 against 50.1).  One tile: 16 per SM (1 token: 14.6 us; DOWN with 6 in a CTA 15.7).
 constexpr int up_warps(int nt) { return nt == 1 ? 16 : 12; }
 constexpr int down_warps(int nt) { return nt == 1 ? 8 : 6; }
 constexpr int along_k(int warps) { return warps == 12 ? 3 : 4; }   // warps of a CTA of UP along K
@@ -238,7 +240,7 @@ __host__ __device__ constexpr int table_bytes(int S, int nblk) {
 }
 
 // Weight of a block of m slots: two token tiles take more instructions, the same loads.  (16 tokens, 2 of 8 experts,
-// 4-bit | 48 tokens, 8-bit: with 4 : 5 120.5 | 83.8 us, 3 : 4 121.3 | 88.3, 2 : 3 129 | 89, 1 : 1 132 | 84.)
+// 4-bit | 48 tokens, 8-bit: with 4 : 5 128.0 | 78.7 us, 3 : 4 128.2 | 82.2, 2 : 3 125.4 | 81.7, 1 : 1 139.8 | 78.2.)
 __device__ __forceinline__ int block_weight(int m) { return m <= 4 ? 4 : 5; }
 
 // Work is dealt out along a line: block u takes `units` of it (UP: its column tiles, DOWN: its fixed-point
@@ -1145,12 +1147,14 @@ void cut_smem(Cut& c, bool up, int T, int S, int E, int Q) {
 // UP: blocks take as many slots, at most 8 and no more than the tokens can fill, as their fixed-point values
 // leave room for (bt = 0: K is too long).
 //  * Few tokens, and no more tiles of 64 values of h than SMs: CTAs of 8 warps, beside which DOWN's start while
-//    they run (1 token, 8 experts of 2048 x 1024: 14.6 us against 17.5 us with 16; with 344 tiles, 2 experts of
-//    4096 x 11008, 54 us against 41.5 us; 4 tokens, 32 experts of 2048 x 1024, 36.6 us against 30.2 us).
+//    they run (1 token, 8 experts of 2048 x 1024: 14.7 us against 18.7 us with 16, of 7168 x 512 27.2 against 32.7; on
+//    an earlier form, with 344 tiles, 2 experts of 4096 x 11008, 54 us against 41.5 us; 4 tokens, 32 experts of
+//    2048 x 1024, 36.6 us against 30.2 us).
 //  * Else one CTA per SM and tiles of 128 values, 3 or 4 warps along K.  (Tiles of 64, where that fills the SMs' last
 //    round better, measured slower on an earlier form: DOWN's shorter fixed-point blocks cost more.  16 tokens, 64
 //    experts of 2048 x 1024: 96 us against 81 us.  So did pairs of CTAs that halve the odd item of their part of the
 //    line: 48 tokens, 8-bit, 99 us against 88 us, though 1 token, 2 experts of 4096 x 11008, took 40 us against 42 us.)
+//  * Very long K with few tokens and short groups, where 16 warps' rings leave no room: 8 warps, one CTA per SM.
 Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
     const int Q = (K + SK - 1) / SK;
     Cut c{};
@@ -1170,7 +1174,7 @@ Cut cut_up(int T, int S, int E, int K, int I, int group_size, int bits) {
         cut_smem(c, true, T, S, E, Q);
         if (c.smem <= max_smem(c.W)) return c;
     }
-    c.W = T <= 4 ? 8 : c.W;   // (T <= 4, K above 20000, short groups: 8 warps, one CTA per SM)
+    c.W = T <= 4 ? 8 : c.W;
     c.bt = 1;
     cut_smem(c, true, T, S, E, Q);
     if (c.smem > WHOLE_SM) c.bt = 0;
