@@ -38,3 +38,22 @@ def test_staged_rows(cuda, libwq, case):
     assert out.intact() and libwq.device_status() == 0
     moe_oracle.assert_close(y, ref, tol, str(case))
     assert torch.equal(libwq.moe(x, ids, weights, *w, bits, G, activation=act, pdl=True), y)
+
+
+@pytest.mark.parametrize("T,E,k,K,I,N,bits,G", [(1, 2, 16, 256, 128, 72, 4, 128), (4, 2, 16, 64, 64, 40, 8, 32),
+                                               (3, 1, 5, 96, 96, 64, 4, 96), (64, 1, 2, 8192, 32, 16, 4, 32),
+                                               (64, 3, 16, 128, 64, 136, 8, -1), (7, 2, 16, 4096, 64, 520, 4, 64)])
+def test_more_slots_than_experts(cuda, libwq, T, E, k, K, I, N, bits, G):
+    """An expert several times among a token's slots, and empty ones between them: blocks of any length."""
+    import torch
+    p = moe_oracle.problem(T, E, 1, K, I, N, bits, G, torch.float16, seed=T + K + k)
+    g = torch.Generator().manual_seed(T + k)
+    p["ids"] = torch.randint(-1, E, (T, k), generator=g).to(torch.int32)
+    p["weights"] = torch.softmax(torch.randn((T, k), generator=g), 1)
+    ref, tol = moe_grouped.layer(p, bits, "silu")
+    (x, ids, weights), w = moe_oracle.to_gpu(libwq, p, bits, cuda)
+    out = Guarded((T, N), x.dtype, cuda)
+    y = libwq.moe(x, ids, weights, *w, bits, G, out=out.view)
+    torch.cuda.synchronize()
+    assert out.intact() and libwq.device_status() == 0
+    moe_oracle.assert_close(y, ref, tol)
